@@ -100,7 +100,7 @@ def _plain_quantize(w, group, symmetric):
         s = (t.abs().amax(2).double() / 7).float().to(torch.bfloat16)
     else:
         lo, hi = t.amin(2).clamp(max=0), t.amax(2).clamp(min=0)
-        s = ((hi - lo).double() / 15).float().to(torch.bfloat16)
+        s = ((hi.double() - lo.double()) / 15).float().to(torch.bfloat16)
     d = s.double()
     safe = torch.where(d == 0, torch.ones_like(d), d)
     z = torch.full_like(d, 8.0) if symmetric else torch.where(d == 0, torch.zeros_like(d), torch.round(-lo.double() / safe).clamp(0, 15))
