@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "api_common.hpp"
 #include "kernels.hpp"
 
 // Fixed scratch of nvfp4_gemm_w4a4_noalloc: one copy on every GPU the
@@ -24,21 +25,11 @@ using namespace nvfp4;
 constexpr int kVersion = 1 * 10000 + 8 * 100 + 1;
 static_assert(kSweepCandidates == NVFP4_SWEEP_CANDIDATES, "candidate count of the activation scale sweep");
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool mul_ok(int64_t a, int64_t b) { return a >= 0 && b >= 0 && (a == 0 || b <= INT64_MAX / a); }
-
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 size_t amax_ws_bytes(int64_t n, bool bf16) {
   return round256(sizeof(float) * (size_t)amax_partial_count(n, bf16));
 }
-
-// Clear a stale error from earlier unrelated work so that a launch failure
-// is attributed to this call.
-void clear_error() { (void)hipGetLastError(); }
-
-int launch_status(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_LAUNCH; }
 
 // Device address of `scratch` on the current device, looked up once per
 // device (with that device current) and kept.  The stream must belong to the
@@ -64,14 +55,6 @@ int noalloc_scratch(hipStream_t stream, void** out) {
   }
   *out = p;
   return NVFP4_OK;
-}
-
-// Calls are not graph-capture safe: refuse a stream that is being captured
-// (before anything is enqueued on it).
-int stream_status(hipStream_t s) {
-  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(s, &cs) != hipSuccess) return NVFP4_ERR_LAUNCH;
-  return cs == hipStreamCaptureStatusNone ? NVFP4_OK : NVFP4_ERR_CAPTURE;
 }
 
 int validate_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, const uint8_t* codes,
