@@ -1,120 +1,197 @@
 // Group-scaled 4-bit integer weights (format: include/int4.h): the quantizer
-// and its inverse.
+// and its inverse.  Both stream: a lane holds 8 consecutive elements (one
+// dword of codes) and a group of 32, 64 or 128 is 4, 8 or 16 neighbouring
+// lanes, so its range is a few lane exchanges.  A wave takes runs of 64
+// vectors of one row; where rows end on a group (the usual case) the whole
+// tensor is one such row.
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
+#include "lanes.hpp"
 
 namespace nvfp4 {
 
-// 8 consecutive elements of row r from column c.
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float v[8]) {
-  if (BF16) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(u[j] << 16);
-      v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-    }
-  } else {
-    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + i);
-    const f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = a[j];
-      v[4 + j] = b[j];
-    }
-  }
+constexpr int kRuns = 4;  // runs of 64 vectors a wave keeps in flight
+
+// The rows a launch sees: the tensor's own, or one of all its elements.
+struct RowView {
+  int64_t rows, n8, padded8;  // vectors of a row, and that rounded up to whole groups
+  int64_t runs;               // runs of 64 vectors of a row
+  int64_t units;              // kRuns runs of a row each
+};
+
+static RowView row_view(int64_t rows, int64_t cols, int group) {
+  RowView v;
+  const bool flat = cols % group == 0;
+  v.rows = flat ? 1 : rows;
+  v.n8 = (flat ? rows * cols : cols) / 8;
+  v.padded8 = (v.n8 + group / 8 - 1) / (group / 8) * (group / 8);
+  v.runs = (v.padded8 + 63) / 64;
+  v.units = (v.runs + kRuns - 1) / kRuns;
+  return v;
 }
 
-// One thread per group.
 template <bool BF16>
-__global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restrict__ x, int64_t slots, int64_t G,
-                                                            int cols, int group, uint8_t* __restrict__ codes,
+struct Raw {
+  u32x4 a[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* x, int64_t vec) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(x) + (BF16 ? vec : 2 * vec);
+    a[0] = __builtin_nontemporal_load(p);
+    if (!BF16) a[BF16 ? 0 : 1] = __builtin_nontemporal_load(p + 1);
+  }
+  __device__ __forceinline__ void zero() {
+    a[0] = u32x4{0, 0, 0, 0};
+    a[BF16 ? 0 : 1] = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if (BF16) return __uint_as_float(j & 1 ? a[0][j / 2] & 0xFFFF0000u : a[0][j / 2] << 16);
+    return __uint_as_float(a[BF16 ? 0 : j / 4][j % 4]);
+  }
+};
+
+// rne(w / s) for |w / s| < 16, given t = w * inv with inv within 2 ulp of
+// 1 / s: t is off by less than 2^-18, so only a t that near to half way
+// between integers needs the exact quotient (fp64: w has 24 significant bits
+// and s 8, so a quotient that is not half way is further from it than fp64
+// rounds).
+constexpr float kHalfway = 0.4999f;
+
+template <bool BF16>
+__global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restrict__ x, RowView rv, int L, int64_t G,
+                                                            uint8_t* __restrict__ codes,
                                                             uint16_t* __restrict__ scales,
                                                             uint8_t* __restrict__ zeros) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < slots; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / G;
-    const int c0 = (int)(i % G) * group, n = min(group, cols - c0);
-    const int64_t base = r * cols + c0;
-    float lo = 0.0f, hi = 0.0f, v[8];
-    for (int c = 0; c < n; c += 8) {
-      load8<BF16>(x, base + c, v);
+  const int lane = threadIdx.x & 63;
+  const int64_t n_units = rv.rows * rv.units;
+  for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
+       u += (int64_t)gridDim.x * 4) {
+    const int64_t row = rv.rows == 1 ? 0 : u / rv.units;
+    const int64_t v0 = (u - row * rv.units) * kRuns * 64 + lane;
+    Raw<BF16> raw[kRuns];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, v[j]);
-        hi = fmaxf(hi, v[j]);
-      }
+    for (int k = 0; k < kRuns; ++k) {
+      if (v0 + 64 * k < rv.n8) raw[k].load(x, row * rv.n8 + v0 + 64 * k);
+      else raw[k].zero();
     }
-    const double range = zeros ? ((double)hi - (double)lo) * (1.0 / 15.0) : (double)fmaxf(hi, -lo) * (1.0 / 7.0);
-    const uint32_t sb = f32_to_bf16_bits((float)range);
-    const double s = (double)bf16_bits_to_f32(sb);
-    double z = zeros ? 0.0 : 8.0;
-    if (zeros && s != 0.0) z = fmin(fmax(__builtin_rint(-(double)lo / s), 0.0), 15.0);
-    scales[i] = (uint16_t)sb;
-    if (zeros) zeros[i] = (uint8_t)(int)z;
-    for (int c = 0; c < n; c += 8) {
-      load8<BF16>(x, base + c, v);
-      uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      const int64_t v = v0 + 64 * k;
+      float lo = 0.0f, hi = 0.0f, w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const double q = s == 0.0 ? z : fmin(fmax(__builtin_rint((double)v[j] / s) + z, 0.0), 15.0);
-        w |= (uint32_t)(int)q << (j < 4 ? 8 * j : 8 * (j - 4) + 4);
+        w[j] = raw[k].at(j);
+        lo = fminf(lo, w[j]);
+        hi = fmaxf(hi, w[j]);
       }
-      *reinterpret_cast<uint32_t*>(codes + (base + c) / 2) = w;
+      lo = lanes_all(lo, L, [](float p, float q) { return fminf(p, q); });
+      hi = lanes_all(hi, L, [](float p, float q) { return fmaxf(p, q); });
+      const double range = zeros ? ((double)hi - (double)lo) * (1.0 / 15.0) : (double)fmaxf(hi, -lo) * (1.0 / 7.0);
+      const uint32_t sb = f32_to_bf16_bits((float)range);
+      const float s = bf16_bits_to_f32(sb);
+      const float inv = __builtin_amdgcn_rcpf(s);
+      const bool odd_scale = s < 0x1p-126f;  // 0 or below the normal range: the estimate does not hold
+      float t[9];                            // the eight quotients, and the zero point's
+      bool near = odd_scale;
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const float q = (j < 8 ? w[j] : -lo) * inv;
+        t[j] = __builtin_rintf(q);
+        near |= fabsf(q - t[j]) > kHalfway;
+      }
+      if (near) {
+#pragma unroll
+        for (int j = 0; j < 9; ++j)
+          t[j] = s == 0.0f ? 0.0f : (float)__builtin_rint((double)(j < 8 ? w[j] : -lo) / (double)s);
+      }
+      const float z = zeros ? __builtin_amdgcn_fmed3f(t[8], 0.0f, 15.0f) : 8.0f;
+      uint32_t word = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float c0 = __builtin_amdgcn_fmed3f(t[b] + z, 0.0f, 15.0f);
+        const float c1 = __builtin_amdgcn_fmed3f(t[4 + b] + z, 0.0f, 15.0f);
+        word |= (uint32_t)__builtin_fmaf(c1, 16.0f, c0) << (8 * b);
+      }
+      if (v < rv.n8) {
+        reinterpret_cast<uint32_t*>(codes)[row * rv.n8 + v] = word;
+        if ((lane & (L - 1)) == 0) {
+          const int64_t slot = row * G + v / L;
+          scales[slot] = (uint16_t)sb;
+          if (zeros) zeros[slot] = (uint8_t)(uint32_t)z;
+        }
+      }
     }
   }
 }
 
-// One thread per dword of 8 codes.
 template <bool BF16>
 __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __restrict__ codes,
                                                            const uint16_t* __restrict__ scales,
-                                                           const uint8_t* __restrict__ zeros, int64_t rows, int64_t G,
-                                                           int cols, int group, void* __restrict__ out) {
-  const int64_t n8 = rows * (cols / 8);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / (cols / 8);
-    const int64_t slot = r * G + (i % (cols / 8)) * 8 / group;
-    const float s = bf16_bits_to_f32(scales[slot]);
-    const int z = zeros ? zeros[slot] : 8;
-    const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
+                                                           const uint8_t* __restrict__ zeros, RowView rv, int L,
+                                                           int64_t G, void* __restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int64_t n_units = rv.rows * rv.units;
+  for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
+       u += (int64_t)gridDim.x * 4) {
+    const int64_t row = rv.rows == 1 ? 0 : u / rv.units;
+    const int64_t v0 = (u - row * rv.units) * kRuns * 64 + lane;
+    uint32_t w[kRuns], sb[kRuns], z[kRuns];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = s * (float)((int)((w >> (j < 4 ? 8 * j : 8 * (j - 4) + 4)) & 15u) - z);
-      if (BF16)
-        reinterpret_cast<uint16_t*>(out)[8 * i + j] = (uint16_t)f32_to_bf16_bits(v);
-      else
-        reinterpret_cast<float*>(out)[8 * i + j] = v;
+    for (int k = 0; k < kRuns; ++k) {
+      const int64_t v = min(v0 + 64 * k, rv.n8 - 1);
+      const int64_t slot = row * G + v / L;
+      w[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes) + row * rv.n8 + v);
+      sb[k] = scales[slot];
+      z[k] = zeros ? zeros[slot] : 8u;
+    }
+#pragma unroll
+    for (int k = 0; k < kRuns; ++k) {
+      const int64_t v = v0 + 64 * k;
+      const float s = bf16_bits_to_f32(sb[k]), zf = (float)z[k];
+      const uint32_t lo = w[k] & 0x0F0F0F0Fu, hi = (w[k] >> 4) & 0x0F0F0F0Fu;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = s * ((float)(((j < 4 ? lo : hi) >> (8 * (j & 3))) & 0xFFu) - zf);
+      if (v >= rv.n8) continue;
+      if (BF16) {
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16_bits(f[2 * j]) | (f32_to_bf16_bits(f[2 * j + 1]) << 16);
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(out) + row * rv.n8 + v);
+      } else {
+        f32x4* o = reinterpret_cast<f32x4*>(out) + 2 * (row * rv.n8 + v);
+        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, o);
+        __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, o + 1);
+      }
     }
   }
 }
 
-static unsigned blocks_of(int64_t n) {
-  const int64_t b = (n + 255) / 256;
-  return (unsigned)(b < (1 << 20) ? b : (1 << 20));
+static dim3 stream_grid(const RowView& v) {
+  const int64_t b = (v.rows * v.units + 3) / 4;
+  return dim3((unsigned)(b < (1 << 20) ? b : (1 << 20)));
 }
 
 hipError_t launch_int4_quantize(const void* x, bool bf16, int64_t rows, int64_t cols, int group, uint8_t* codes,
                                 uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const int64_t G = (cols + group - 1) / group, slots = rows * G;
-  if (bf16)
-    hipLaunchKernelGGL(int4_quantize_kernel<true>, dim3(blocks_of(slots)), dim3(256), 0, stream, x, slots, G, (int)cols,
-                       group, codes, scales, zeros);
-  else
-    hipLaunchKernelGGL(int4_quantize_kernel<false>, dim3(blocks_of(slots)), dim3(256), 0, stream, x, slots, G,
-                       (int)cols, group, codes, scales, zeros);
+  const RowView v = row_view(rows, cols, group);
+  const int64_t G = (cols + group - 1) / group;
+#define INT4_QUANTIZE(B) \
+  hipLaunchKernelGGL(int4_quantize_kernel<B>, stream_grid(v), dim3(256), 0, stream, x, v, group / 8, G, codes, scales, zeros)
+  if (bf16) INT4_QUANTIZE(true);
+  else INT4_QUANTIZE(false);
+#undef INT4_QUANTIZE
   return hipGetLastError();
 }
 
 hipError_t launch_int4_dequant(const Int4Weight& w, int64_t rows, int64_t cols, void* out, bool bf16_out,
                                hipStream_t stream) {
-  const int64_t G = (cols + w.group - 1) / w.group, n8 = rows * (cols / 8);
-  if (bf16_out)
-    hipLaunchKernelGGL(int4_dequant_kernel<true>, dim3(blocks_of(n8)), dim3(256), 0, stream, w.codes, w.scales,
-                       w.zeros, rows, G, (int)cols, w.group, out);
-  else
-    hipLaunchKernelGGL(int4_dequant_kernel<false>, dim3(blocks_of(n8)), dim3(256), 0, stream, w.codes, w.scales,
-                       w.zeros, rows, G, (int)cols, w.group, out);
+  const RowView v = row_view(rows, cols, w.group);
+  const int64_t G = (cols + w.group - 1) / w.group;
+#define INT4_DEQUANT(B)                                                                                       \
+  hipLaunchKernelGGL(int4_dequant_kernel<B>, stream_grid(v), dim3(256), 0, stream, w.codes, w.scales, w.zeros, v, \
+                     w.group / 8, G, out)
+  if (bf16_out) INT4_DEQUANT(true);
+  else INT4_DEQUANT(false);
+#undef INT4_DEQUANT
   return hipGetLastError();
 }
 

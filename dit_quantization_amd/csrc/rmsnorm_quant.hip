@@ -1,91 +1,267 @@
 // Residual addition, RMS norm and 8-bit output with scales (definition:
-// include/int4.h, int4_rmsnorm_quant8).
+// include/int4.h, int4_rmsnorm_quant8): h = x + r, y = h w / sqrt(mean h^2 +
+// eps), s = max|y| / Q, code = round(y / s).
+//
+// One pass over memory: a team of T threads holds a row of h in registers
+// (vectors of 8 columns, V a thread, thread t has vectors t, t + T, ...), adds
+// up h^2 and takes the maximum of |h w|, neither of which needs the norm, and
+// after one exchange multiplies h w by inv / s.  Groups of 32, 64 and 128
+// columns are 4, 8 and 16 neighbouring lanes.
+//
+// A code is the nearest to the exact y / s, so sums, products and quotients
+// are fp64: the fp64 pipe runs at the fp32 rate on this chip, and the dozen
+// operations an element takes fit under the 7 bytes it moves.
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
+#include "lanes.hpp"
 
 namespace nvfp4 {
 
-// Nearest E4M3 byte to v (ties to even, saturating at 448), rounded once:
-// the low half of the fp64 value becomes a sticky bit, which leaves 21
-// significant bits that convert to fp32 exactly, and the converter rounds.
+enum class Res { kNone, kBf16, kF32 };
+
+// The value with its low 32 bits folded into a sticky bit: 21 significant
+// bits, which convert to fp32 exactly, so that a later rounding to 8 bits is
+// the only one.
 __device__ __forceinline__ float sticky_f32(double v) {
-  const uint64_t b = __double_as_longlong(v);
-  const uint32_t hi = (uint32_t)(b >> 32) | ((uint32_t)b != 0u ? 1u : 0u);
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t hi = (uint32_t)(b >> 32) | min((uint32_t)b, 1u);
   return (float)__longlong_as_double((int64_t)((uint64_t)hi << 32));
 }
 
-__device__ __forceinline__ float norm_load(const void* p, int64_t i, bool bf16) {
-  return bf16 ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+// 1 / x and 1 / sqrt(x) for positive normal x: the hardware estimate and two
+// Newton steps (each squares the error).
+__device__ __forceinline__ double rcp64(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(y, __builtin_fma(-x, y, 1.0), y);
+  return y;
+}
+__device__ __forceinline__ double rsqrt64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(y, __builtin_fma(-0.5 * x * y, y, 0.5), y);
+  return y;
 }
 
-// One workgroup per row; three passes over its elements.
-__global__ __launch_bounds__(256) void rmsnorm_quant_kernel(NormArgs a) {
-  __shared__ double red[256];
-  const int t = threadIdx.x;
-  const int step = a.group ? a.group : a.cols, G = (a.cols + step - 1) / step;
-  const double top = a.e4m3 ? 448.0 : 127.0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    auto h_at = [&](int c) {
-      const float x = norm_load(a.x, r * a.x_stride + c, a.x_bf16);
-      if (!a.residual) return x;
-      const float h = x + norm_load(a.residual, r * a.res_stride + c, a.res_bf16);
-      return a.res_bf16 ? bf16_bits_to_f32(f32_to_bf16_bits(h)) : h;
-    };
-    auto y_at = [&](int c) { return (double)h_at(c) * (a.weight ? (double)norm_load(a.weight, c, a.w_bf16) : 1.0); };
-    double ss = 0.0;
-    for (int c = t; c < a.cols; c += 256) ss += (double)h_at(c) * (double)h_at(c);
-    red[t] = ss;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-      if (t < o) red[t] += red[t + o];
-      __syncthreads();
+// 8 columns as they lie in memory, bf16 or fp32.
+template <bool BF16>
+struct Vec8 {
+  u32x4 a[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4* q = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(p) + i * (BF16 ? 2 : 4));
+    a[0] = q[0];
+    if (!BF16) a[BF16 ? 0 : 1] = q[1];
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    u32x4* q = reinterpret_cast<u32x4*>(reinterpret_cast<char*>(p) + i * (BF16 ? 2 : 4));
+    q[0] = a[0];
+    if (!BF16) q[1] = a[BF16 ? 0 : 1];
+  }
+  __device__ __forceinline__ void zero() {
+    a[0] = u32x4{0, 0, 0, 0};
+    a[BF16 ? 0 : 1] = u32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if (BF16) return __uint_as_float(j & 1 ? a[0][j / 2] & 0xFFFF0000u : a[0][j / 2] << 16);
+    return __uint_as_float(a[BF16 ? 0 : j / 4][j % 4]);
+  }
+  __device__ __forceinline__ void set(const float v[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!BF16) a[BF16 ? 0 : j / 4][j % 4] = __float_as_uint(v[j]);
+      else if (j & 1) a[0][j / 2] = f32_to_bf16_bits(v[j - 1]) | (f32_to_bf16_bits(v[j]) << 16);
     }
-    const double inv = 1.0 / sqrt(red[0] / a.cols + a.eps);
-    __syncthreads();
-    for (int g = 0; g < G; ++g) {
-      const int c0 = g * step, c1 = min(c0 + step, a.cols);
-      double m = 0.0;
-      for (int c = c0 + t; c < c1; c += 256) m = fmax(m, fabs(y_at(c)));
-      red[t] = m;
-      __syncthreads();
-      for (int o = 128; o > 0; o >>= 1) {
-        if (t < o) red[t] = fmax(red[t], red[t + o]);
-        __syncthreads();
-      }
-      m = red[0];
-      __syncthreads();
-      float s = m > 0.0 ? (float)(m * inv / top) : 0.0f;
-      if (s == 0.0f) s = 1.0f;
-      if (t == 0) a.scales[r * G + g] = s;
-      const double k = m > 0.0 ? inv / (double)s : 0.0;
-      for (int c = c0 + t; c < c1; c += 256) {
-        const double v = y_at(c) * k;
-        uint32_t q;
-        if (a.e4m3) {
-          const float f = fminf(fmaxf(sticky_f32(v), -448.0f), 448.0f);
-          q = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f, f, 0, false) & 0xFFu;
-        } else {
-          q = (uint32_t)(int)fmin(fmax(__builtin_rint(v), -127.0), 127.0) & 0xFFu;
-        }
-        reinterpret_cast<uint8_t*>(a.codes)[r * a.cols + c] = (uint8_t)q;
-      }
-    }
-    __syncthreads();
-    if (a.residual)
-      for (int c = t; c < a.cols; c += 256) {
-        const float h = h_at(c);
-        if (a.res_bf16)
-          reinterpret_cast<uint16_t*>(a.residual_out)[r * a.cols + c] = (uint16_t)(__float_as_uint(h) >> 16);
-        else
-          reinterpret_cast<float*>(a.residual_out)[r * a.cols + c] = h;
-      }
+  }
+};
+
+__device__ __forceinline__ void load_weight(const NormArgs& a, int i, float w[8]) {
+  if (!a.weight) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+  } else if (a.w_bf16) {
+    Vec8<true> v;
+    v.load(a.weight, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = v.at(j);
+  } else {
+    Vec8<false> v;
+    v.load(a.weight, i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = v.at(j);
   }
 }
 
-hipError_t launch_rmsnorm_quant8(const NormArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20)));
-  hipLaunchKernelGGL(rmsnorm_quant_kernel, grid, dim3(256), 0, stream, a);
+// 8 codes of y / s = p k as two dwords.
+__device__ __forceinline__ u32x2 encode_i8(const double p[8], double k) {
+  u32x2 q;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // adding 1.5 2^52 rounds to the nearest integer, ties to even, and
+      // leaves it in the low bits
+      const double r = __builtin_fma(p[4 * d + j], k, 6755399441055744.0);
+      const int c = min(max((int)__double_as_longlong(r), -127), 127);
+      w |= ((uint32_t)c & 0xFFu) << (8 * j);
+    }
+    q[d] = w;
+  }
+  return q;
+}
+__device__ __forceinline__ u32x2 encode_e4m3(const double p[8], double k) {
+  u32x2 q;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    float f[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __builtin_amdgcn_fmed3f(sticky_f32(p[4 * d + j] * k), -448.0f, 448.0f);
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    q[d] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
+  }
+  return q;
+}
+
+template <int T, int V, bool XBF, Res RES>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_quant_kernel(NormArgs a, double inv_cols, double inv_top) {
+  constexpr int B = T < 256 ? 256 : T, TEAMS = B / T, NW = T / 64;
+  __shared__ double red[2][16];
+  const int t = threadIdx.x % T;
+  const int64_t r = (int64_t)blockIdx.x * TEAMS + threadIdx.x / T;
+  const int n8 = a.cols / 8;
+  const bool live_row = r < a.rows;
+  // The weight is read again for the codes where a thread has many vectors
+  // (an L1 or L2 hit; the registers are worth more).
+  constexpr bool kKeep = V <= 2;
+  constexpr bool HBF = RES == Res::kNone ? XBF : RES == Res::kBf16;
+  Vec8<HBF> h[V];
+  float w[kKeep ? V : 1][8];
+  double ss = 0.0, m[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = t + T * v;
+    float* const wv = w[kKeep ? v : 0];
+    h[v].zero();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wv[j] = 0.0f;
+    if (live_row && i < n8) {
+      if constexpr (RES == Res::kNone) {
+        h[v].load(a.x, r * a.x_stride + 8 * i);
+      } else {
+        Vec8<XBF> x;
+        x.load(a.x, r * a.x_stride + 8 * i);
+        h[v].load(a.residual, r * a.res_stride + 8 * i);
+        float sum[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = x.at(j) + h[v].at(j);
+        h[v].set(sum);
+        h[v].store(a.residual_out, r * a.cols + 8 * i);
+      }
+      load_weight(a, 8 * i, wv);
+    }
+    m[v] = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double d = (double)h[v].at(j);
+      ss = __builtin_fma(d, d, ss);
+      m[v] = fmax(m[v], fabs(d * (double)wv[j]));
+    }
+  }
+  const auto add = [](double p, double q) { return p + q; };
+  const auto most = [](double p, double q) { return fmax(p, q); };
+  double all = 0.0;  // the row's maximum
+  if (a.group == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) all = fmax(all, m[v]);
+  }
+  if (T == 16) {
+    ss = lanes_all<16>(ss, add);
+    if (a.group == 0) all = lanes_all<16>(all, most);
+  } else {
+    ss = lanes_all<64>(ss, add);
+    if (a.group == 0) all = lanes_all<64>(all, most);
+  }
+  if (T > 64) {
+    // 4 (16) waves: every lane reads the partial results, which the lanes of
+    // a quad (of a run of 16) then combine in the same way everywhere
+    const int wave = threadIdx.x / 64;
+    if (threadIdx.x % 64 == 0) {
+      red[0][wave] = ss;
+      red[1][wave] = all;
+    }
+    __syncthreads();
+    ss = red[0][threadIdx.x % NW];
+    ss = NW == 4 ? lanes_all<4>(ss, add) : lanes_all<16>(ss, add);
+    if (a.group == 0) {
+      all = red[1][threadIdx.x % NW];
+      all = NW == 4 ? lanes_all<4>(all, most) : lanes_all<16>(all, most);
+    }
+  }
+  const double ms = __builtin_fma(ss, inv_cols, a.eps);
+  const double inv = ms > 0.0 ? rsqrt64(ms) : 0.0;
+  const int L = a.group / 8, G = a.group ? (a.cols + a.group - 1) / a.group : 1;
+  // scale, and the factor that turns h w into y / s (0 where all is 0)
+  const auto scale_of = [&](double top, float& s) {
+    s = (float)(top * inv * inv_top);
+    if (s == 0.0f) s = 1.0f;
+    return inv * rcp64((double)s);
+  };
+  float s_row = 1.0f;
+  double k = 0.0;
+  if (a.group == 0) {
+    k = scale_of(all, s_row);
+    if (t == 0 && live_row) a.scales[r] = s_row;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = t + T * v;
+    if (a.group) {
+      float s;
+      k = scale_of(lanes_all(m[v], L, most), s);
+      if (live_row && i < n8 && (i & (L - 1)) == 0) a.scales[r * G + i / L] = s;
+    }
+    if (live_row && i < n8) {
+      float* const wv = w[kKeep ? v : 0];
+      if (!kKeep) load_weight(a, 8 * i, wv);
+      double p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = (double)h[v].at(j) * (double)wv[j];
+      const u32x2 q = a.e4m3 ? encode_e4m3(p, k) : encode_i8(p, k);
+      *reinterpret_cast<u32x2*>(reinterpret_cast<uint8_t*>(a.codes) + r * a.cols + 8 * i) = q;
+    }
+  }
+}
+
+template <bool XBF, Res RES>
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  const int n8 = a.cols / 8;
+  const double ic = 1.0 / a.cols, it = a.e4m3 ? 1.0 / 448.0 : 1.0 / 127.0;
+#define NORM_CASE(T, V)                                                                                                \
+  hipLaunchKernelGGL((rmsnorm_quant_kernel<T, V, XBF, RES>),                                                            \
+                     dim3((unsigned)((a.rows + (T < 256 ? 256 / T : 1) - 1) / (T < 256 ? 256 / T : 1))),               \
+                     dim3(T < 256 ? 256 : T), 0, stream, a, ic, it)
+  if (n8 <= 16) NORM_CASE(16, 1);
+  else if (n8 <= 64) NORM_CASE(64, 1);
+  else if (n8 <= 256) NORM_CASE(256, 1);
+  else if (a.rows <= 256 || n8 > 2048) {
+    // few rows: short loops in wide teams; also rows too long for 256 threads
+    if (n8 <= 1024) NORM_CASE(1024, 1);
+    else if (n8 <= 2048) NORM_CASE(1024, 2);
+    else if (n8 <= 4096) NORM_CASE(1024, 4);
+    else NORM_CASE(1024, 8);
+  } else {
+    if (n8 <= 512) NORM_CASE(256, 2);
+    else if (n8 <= 1024) NORM_CASE(256, 4);
+    else NORM_CASE(256, 8);
+  }
+#undef NORM_CASE
   return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_quant8(const NormArgs& a, hipStream_t stream) {
+  if (!a.residual) return a.x_bf16 ? launch_norm<true, Res::kNone>(a, stream) : launch_norm<false, Res::kNone>(a, stream);
+  if (a.res_bf16) return launch_norm<true, Res::kBf16>(a, stream);
+  return a.x_bf16 ? launch_norm<true, Res::kF32>(a, stream) : launch_norm<false, Res::kF32>(a, stream);
 }
 
 }  // namespace nvfp4
