@@ -15,6 +15,8 @@ namespace nvfp4 {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kPassSupers = 4;  // super-chunks of 128 codes a pass of the matrix kernel takes
+
 // What a product of bytes has to be multiplied by.
 template <Act A>
 constexpr float kUnit = A == Act::kI8 ? 1.0f : 512.0f;
@@ -183,16 +185,28 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // A workgroup of NW waves owns 16 T weight rows; its waves split K into runs
 // of super-chunks of 128 codes, 4 to a pass.  The codes of a pass reach LDS by
 // DMA, every instruction reading 4 rows x 256 contiguous bytes, and lane
-// (n, g) (n = lane % 16, g = lane / 16) reads back the 32 codes of chunk
-// 4 s + g of row n from a row-swizzled slot.  A matrix instruction adds up
-// over the lane groups g, so the codes it takes must be of one scale group:
-// with groups of 128 those are the four lanes' chunks as they are; for 64 and
-// 32 the dwords trade places between lane groups (v_permlane32_swap,
-// v_permlane16_swap: a step each of a 4 x 4 transpose), after which
-// instruction j covers chunks 2 (j / 2) + {0, 1}, or chunk j alone.  A
-// product of one scale group starts at zero and is added into the fp32 sums
-// with its scale, z taken off with the sums of x (one more matrix product
-// with a constant operand, shared by the T row tiles).
+// (n, g) (n = lane % 16, g = lane / 16) reads back the 32 codes of one chunk
+// of row n from a row-swizzled slot.  A matrix instruction adds up over the
+// lane groups g, and which 8 of the 128 codes each group feeds it is free as
+// long as x agrees and all 32 belong to one scale group: 8 each for bf16 and
+// groups of 32 (instruction j takes chunk j), 16 each for two instructions of
+// 8-bit activations (j / 2 takes half a super-chunk).  The dwords of the codes
+// trade places between lane groups accordingly (v_permlane16_swap and
+// v_permlane32_swap, one or two steps of a 4 x 4 transpose).
+//
+// Reading x costs as much as reading the codes: every workgroup reads all of
+// it, from L2, and a load instruction takes the same 16 cycles of the address
+// path whether its lanes are live or not.  So x is read like the codes, 4
+// rows x 256 contiguous bytes an instruction and none for rows past M, and
+// put into the operands' layout through LDS.  (Loads straight into that
+// layout, 16 rows x 64 bytes, meet on few L2 channels where K is a large power
+// of two: 14336 x 4096 at M = 16, bf16, took 11.6 us instead of 10.6.)  So are
+// the scales, which the four lane groups would otherwise each load (8.5 us
+// instead of 9.0 on that weight at M = 1).
+//
+// A product of one scale group starts at zero and is added into the fp32 sums with its scale, z taken off with the
+// sums of x (one more matrix product with a constant operand, shared by the T
+// row tiles).
 //
 // E4M3 activations are widened to bf16 as well: the FP8 matrix instruction
 // keeps too few bits of its sums (9e-5 off, relative, after 160 products,
@@ -201,7 +215,6 @@ template <Act A>
 struct Mfma {
   using Acc = f32x4;
   using X = u32x4;   // 8 bf16
-  static constexpr int kBytes = A == Act::kBf16 ? 16 : 8;  // of 8 activations in memory
   static __device__ __forceinline__ Acc mul(X x, X w, Acc c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0, 0,
                                                    0);
@@ -210,77 +223,106 @@ struct Mfma {
     return X{pk_bf16_e4m3(a, false), pk_bf16_e4m3(a, true), pk_bf16_e4m3(b, false), pk_bf16_e4m3(b, true)};
   }
   static __device__ __forceinline__ X unpack(uint32_t w) { return bytes(w & kNibbles, (w >> 4) & kNibbles); }
-  static __device__ __forceinline__ X load(__amdgpu_buffer_rsrc_t buf, int off) {
-    if constexpr (A == Act::kBf16) {
-      return __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0);
-    } else {
-      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(buf, off, 0, 0);
-      return bytes(v.x, v.y);
-    }
-  }
+  static __device__ __forceinline__ X of(u32x2 v) { return bytes(v.x, v.y); }
   static __device__ __forceinline__ X ones() { return X{0x3B003B00u, 0x3B003B00u, 0x3B003B00u, 0x3B003B00u}; }
 };
 template <>
 struct Mfma<Act::kI8> {
   using Acc = i32x4;
   using X = u32x2;
-  static constexpr int kBytes = 8;
   static __device__ __forceinline__ Acc mul(X x, X w, Acc c) {
     return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, x), __builtin_bit_cast(long, w), c, 0, 0, 0);
   }
   static __device__ __forceinline__ X unpack(uint32_t w) { return X{w & kNibbles, (w >> 4) & kNibbles}; }
-  static __device__ __forceinline__ X load(__amdgpu_buffer_rsrc_t buf, int off) {
-    return __builtin_amdgcn_raw_buffer_load_b64(buf, off, 0, 0);
-  }
+  static __device__ __forceinline__ X of(u32x2 v) { return v; }
   static __device__ __forceinline__ X ones() { return X{0x01010101u, 0x01010101u}; }
 };
 
-// The dwords of lane (n, g)'s chunk become those its matrix instructions
-// j = 0..3 take (see above).
-template <int GS>
+// Bits of a code's place: lane group g = (g1, g0), dword d = (d1, d0) of its
+// chunk.  In pairs: lane group g reads chunk (g0, g1), and trading g0 with d1
+// leaves instruction j = (j1, j0) with dword 2 g + j0 of half super-chunk j1.
+// One by one: lane group g reads chunk g, and trading both bits leaves
+// instruction j with dword g of chunk j.
+template <bool PAIRS>
+__device__ __forceinline__ int chunk_of(int g) { return PAIRS ? 2 * (g & 1) + (g >> 1) : g; }
+
+template <bool PAIRS>
 __device__ __forceinline__ u32x4 regroup(u32x4 d) {
-  if constexpr (GS <= 64) {
+  if constexpr (PAIRS) {
+    const auto a = __builtin_amdgcn_permlane16_swap(d[0], d[2], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(d[1], d[3], false, false);
+    return u32x4{a[0], b[0], a[1], b[1]};
+  } else {
     const auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
     const auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
-    d = u32x4{a[0], b[0], a[1], b[1]};
+    const auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{e[0], e[1], f[0], f[1]};
   }
-  if constexpr (GS == 32) {
-    const auto a = __builtin_amdgcn_permlane16_swap(d[0], d[1], false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(d[2], d[3], false, false);
-    d = u32x4{a[0], a[1], b[0], b[1]};
-  }
-  return d;
 }
 
-template <int G>
-__device__ __forceinline__ void wait_newer(int k) {
-  if (k == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-  else if (k == 1) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(G));
-  else if (k == 2) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(2 * G));
-  else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(3 * G));
+// LDS written by other lanes of the wave is read after this (a wave's LDS
+// operations complete in order: only the compiler has to keep it).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
-template <Act A, int GS, int T, int NW>
+// What a wave loads into registers for one pass; all of it goes through LDS
+// to the lanes that need it (loads in the operands' layout would be more
+// instructions of fewer live lanes each).
+template <Act A, bool GX, int GS, int T, int MQ>
+struct Pass {
+  static constexpr int XB = A == Act::kBf16 ? 2 : 1;  // bytes of an activation
+  static constexpr int XR = 2 * XB;                   // rounds of 16 rows x 256 bytes that x goes through LDS in
+  static constexpr int NG = kPassSupers * 128 / GS;   // scale groups
+  static constexpr int SI = (16 * T * NG / 4 + 63) / 64;
+  u32x4 x[XR][MQ];   // x: 4 MQ rows
+  u32x2 s[SI];       // scales of 4 groups of a row: item i = 64 a + lane is row i % 16T, groups 4 (i / 16T)..
+  uint32_t z[SI];    // and their zero points
+  float f[GX ? NG / 4 : 1];  // grouped scales of x: row lane % 16, group 4 a + lane / 16
+};
+
+// GX: x has a scale for each group.  MQ: 4 MQ rows of x are read (M <= 4 MQ).
+template <Act A, bool GX, int GS, int T, int NW, int MQ>
 __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4Weight w, int M, int N, int K, int G,
                                                                  int wide, void* __restrict__ y, int bf16_out) {
   using Op = Mfma<A>;
   using Acc = typename Op::Acc;
-  constexpr int SW = 4;           // super-chunks per pass
-  constexpr int PER = 128 / GS;   // scale groups of a super-chunk
-  constexpr int NG = SW * PER;    // and of a pass
-  __shared__ u32x4 lds_c[NW][T][256];
+  using P = Pass<A, GX, GS, T, MQ>;
+  constexpr int SW = kPassSupers, XB = P::XB, XR = P::XR, NG = P::NG;
+  constexpr int PER = 128 / GS;                       // scale groups of a super-chunk
+  constexpr bool PAIRS = A != Act::kBf16 && GS >= 64;
+  constexpr int R = 16 * T;                           // rows of the workgroup
+  static_assert(T <= 4, "one LDS array per tile");
+  // One array per row tile: the compiler then knows which DMA a read depends
+  // on and waits for that one only (with one array for all tiles the first
+  // tile's reads waited for every DMA in flight: 14336 x 4096, M = 16, INT8,
+  // 9.8 us instead of 9.2).
+  __shared__ u32x4 lds_c0[NW][256], lds_c1[NW][256], lds_c2[NW][256], lds_c3[NW][256];
+  __shared__ u32x4 lds_x[NW][256];
+  __shared__ uint32_t lds_s[NW][T == 1 ? 28 * NG : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const auto tile = [&](int t) {  // t is a constant once the loops are unrolled
+    return t == 0 ? lds_c0[wave] : t == 1 ? lds_c1[wave] : t == 2 ? lds_c2[wave] : lds_c3[wave];
+  };
+  // Scales [NG / 4][R] pairs of dwords, zero points [NG / 4][R], grouped scales
+  // of x [NG][16]; with several tiles in the place of x, which is in registers
+  // by then.
+  uint32_t* const st_s = T == 1 ? lds_s[wave] : reinterpret_cast<uint32_t*>(lds_x[wave]);
+  uint32_t* const st_z = st_s + R * NG / 2;
+  float* const st_f = reinterpret_cast<float*>(st_z + R * NG / 4);
+  static_assert(T == 1 || (R * NG * 3 / 4 + 16 * NG) * 4 <= 4096, "scales fit the place of x");
   const int nl = lane & 15, g = lane >> 4;
   const int n0 = (int)blockIdx.x * (16 * T);
-  const int rows = min(16 * T, N - n0);
+  const int rows = min(R, N - n0);
   const int half = K / 2;
   const __amdgpu_buffer_rsrc_t cbuf = make_buf(w.codes + (int64_t)n0 * half, (uint32_t)(rows * half));
   const __amdgpu_buffer_rsrc_t sbuf = make_buf(w.scales + (int64_t)n0 * G, (uint32_t)(rows * G * 2));
   const __amdgpu_buffer_rsrc_t zbuf = make_buf(w.zeros ? w.zeros + (int64_t)n0 * G : nullptr,
                                                w.zeros ? (uint32_t)(rows * G) : 0u);
-  const __amdgpu_buffer_rsrc_t xbuf = make_buf(x.x, (uint32_t)(M * K * (Op::kBytes / 8)));
-  const bool grouped = A != Act::kBf16 && x.grouped;
-  const __amdgpu_buffer_rsrc_t fbuf = make_buf(x.scales, grouped ? (uint32_t)(M * G * 4) : 0u);
+  const __amdgpu_buffer_rsrc_t xbuf = make_buf(x.x, (uint32_t)(M * K * XB));
+  const __amdgpu_buffer_rsrc_t fbuf = make_buf(x.scales, GX ? (uint32_t)(M * G * 4) : 0u);
   const int nch = K / 32, nsc = (nch + 3) / 4;
   const int per = ((nsc + NW - 1) / NW + SW - 1) / SW * SW;  // whole passes, so scales are read in aligned runs
   const int sbeg = wave * per, send = min(sbeg + per, nsc);
@@ -289,79 +331,127 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
 #pragma unroll
   for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int s0 = sbeg; s0 < send; s0 += SW) {  // wave-uniform
-    // x (L2 hits), then scales, then codes, so that what comes first is waited for first
-    typename Op::X xa[SW][4];
+  // Byte offsets of this lane's loads at super-chunk 0.
+  int x_at[MQ], c_at[SW];
 #pragma unroll
-    for (int u = 0; u < SW; ++u) {
+  for (int q = 0; q < MQ; ++q) {
+    const int row = 4 * q + g;
+    x_at[q] = row < M ? row * K * XB + 16 * nl : kBufOOB;
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // the codes instruction j has from lane group g
-        const int chunk = 4 * (s0 + u) + (GS == 128 ? g : GS == 64 ? 2 * (j >> 1) + (g & 1) : j);
-        const int dword = GS == 128 ? j : GS == 64 ? 2 * (g >> 1) + (j & 1) : g;
-        const bool ok = nl < M && chunk < nch && s0 + u < send;
-        const int off = ok ? nl * (K * (Op::kBytes / 8)) + Op::kBytes * (4 * chunk + dword) : kBufOOB;
-        xa[u][j] = Op::load(xbuf, off);
-      }
-    }
+  for (int u = 0; u < SW; ++u) {
+    const int r = 4 * u + g;
+    c_at[u] = r * half + 16 * (nl ^ r);
+  }
+  const auto dma = [&](int t, int u, int off) {
+    // non-temporal: each code byte is read once
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        cbuf, (__attribute__((address_space(3))) void*)(tile(t) + 64 * u), 16, off, 0, 0, kBufNT);
+  };
+  // The loads of the pass from super-chunk s0: x (L2 hits), then scales, then
+  // codes, so that what comes first is waited for first.  x comes 4 rows x 256
+  // contiguous bytes an instruction; DMA instruction u of tile t fills LDS
+  // slots [64 u, 64 u + 64): lane l -> row r = 4 u + l / 16, slot j = l % 16,
+  // holding chunk 4 s0 + (j ^ r).  
+  const auto load = [&](P& p, int s0) {
     const int g0 = s0 * PER;  // first scale group of the pass
-    uint32_t sw[T][NG / 2], zw[T][NG / 4];
+    if (wide && s0 + SW <= send) {
+      // K % 512 == 0 and aligned pointers: the whole pass lies inside the rows
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const int base = (16 * t + nl) * G + g0;
-      if (wide) {  // K % 512 == 0 and aligned pointers: the pass's groups lie inside the row
+      for (int v = 0; v < XR; ++v)
 #pragma unroll
-        for (int q = 0; q < NG / 4; ++q) {
-          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(sbuf, 2 * base + 8 * q, 0, 0);
-          sw[t][2 * q] = v.x;
-          sw[t][2 * q + 1] = v.y;
-          zw[t][q] = w.zeros ? __builtin_amdgcn_raw_buffer_load_b32(zbuf, base + 4 * q, 0, 0) : 0x08080808u;
+        for (int q = 0; q < MQ; ++q)
+          p.x[v][q] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, x_at[q] + 128 * XB * s0, 256 * v, 0);
+#pragma unroll
+      for (int a = 0; a < P::SI; ++a) {
+        const int item = 64 * a + lane;
+        const int base = R * NG / 4 % 64 == 0 || item < R * NG / 4 ? item % R * G + g0 + 4 * (item / R) : kBufOOB / 2;
+        p.s[a] = __builtin_amdgcn_raw_buffer_load_b64(sbuf, 2 * base, 0, 0);
+        p.z[a] = w.zeros ? __builtin_amdgcn_raw_buffer_load_b32(zbuf, base, 0, 0) : 0x08080808u;
+      }
+      if constexpr (GX) {
+#pragma unroll
+        for (int a = 0; a < NG / 4; ++a)
+          p.f[a] = __builtin_bit_cast(
+              float, __builtin_amdgcn_raw_buffer_load_b32(fbuf, 4 * (nl * G + g0 + 4 * a + g), 0, 0));
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        __builtin_amdgcn_sched_barrier(0);  // tile order
+#pragma unroll
+        for (int u = 0; u < SW; ++u) dma(t, u, c_at[u] + 16 * t * half + 64 * s0);
+      }
+    } else {
+      // any K: what lies past K or this wave's range reads as zero
+      const int kend = min(K, 128 * send);
+#pragma unroll
+      for (int v = 0; v < XR; ++v)
+#pragma unroll
+        for (int q = 0; q < MQ; ++q) {
+          const int k = 128 * s0 + (256 * v + 16 * nl) / XB;
+          p.x[v][q] = __builtin_amdgcn_raw_buffer_load_b128(
+              xbuf, k < kend ? x_at[q] + 128 * XB * s0 + 256 * v : kBufOOB, 0, 0);
         }
-      } else {
 #pragma unroll
-        for (int q = 0; q < NG / 2; ++q) sw[t][q] = 0;
+      for (int a = 0; a < P::SI; ++a) {
+        const int item = 64 * a + lane, row = item % R, gq = g0 + 4 * (item / R);
+        uint32_t s[4], z = 0;
 #pragma unroll
-        for (int q = 0; q < NG / 4; ++q) zw[t][q] = 0;
+        for (int q = 0; q < 4; ++q) {
+          const int at = item < R * NG / 4 && gq + q < G ? row * G + gq + q : kBufOOB / 2;
+          s[q] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf, 2 * at, 0, 0) & 0xFFFFu;
+          z |= (w.zeros ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf, at, 0, 0) & 0xFFu : 8u) << (8 * q);
+        }
+        p.s[a] = u32x2{s[0] | (s[1] << 16), s[2] | (s[3] << 16)};
+        p.z[a] = z;
+      }
+      if constexpr (GX) {
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          const bool ok = g0 + q < G;
-          sw[t][q / 2] |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf, ok ? 2 * (base + q) : kBufOOB, 0, 0)
-                          << (16 * (q & 1));
-          zw[t][q / 4] |= (w.zeros ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf, ok ? base + q : kBufOOB, 0, 0) : 8u)
-                          << (8 * (q & 3));
+        for (int a = 0; a < NG / 4; ++a) {
+          const int q = g0 + 4 * a + g;
+          p.f[a] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                 fbuf, q < G ? 4 * (nl * G + q) : kBufOOB, 0, 0));
         }
       }
-    }
-    float fx[NG][4];
-    if (grouped) {
 #pragma unroll
-      for (int q = 0; q < NG; ++q)
+      for (int t = 0; t < T; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          fx[q][i] = __builtin_bit_cast(
-              float, __builtin_amdgcn_raw_buffer_load_b32(
-                         fbuf, 4 * g + i < M && g0 + q < G ? 4 * ((4 * g + i) * G + g0 + q) : kBufOOB, 0, 0));
-    }
-    // DMA instruction u of tile t fills LDS slots [64 u, 64 u + 64): lane l ->
-    // row r = 4 u + l / 16, slot j = l % 16, holding chunk 4 s0 + (j ^ r).
-    // Chunks past this wave's range, or past K, read as zero.
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      __builtin_amdgcn_sched_barrier(0);  // tile order
-#pragma unroll
-      for (int u = 0; u < SW; ++u) {
-        const int r = 4 * u + (lane >> 4);
-        const int c = 4 * s0 + ((lane & 15) ^ r);
-        const bool ok = c < 4 * send && c < nch;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(cbuf, (__attribute__((address_space(3))) void*)&lds_c[wave][t][64 * u],
-                                                 16, ok ? (16 * t + r) * half + 16 * c : kBufOOB, 0, 0, kBufNT);
+        for (int u = 0; u < SW; ++u)
+          dma(t, u, 4 * s0 + (nl ^ (4 * u + g)) < min(nch, 4 * send) ? c_at[u] + 16 * t * half + 64 * s0 : kBufOOB);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    // sums of x over each scale group, for this lane's rows 4 g + i
-    f32x4 xs[NG];
+  };
+
+  // x of round v through LDS into the operands' layout: piece p (16 bytes) of
+  // row r lies in slot p ^ r of the row, so neither side has bank conflicts.
+  // Rows past 4 MQ are not written; what is read there only reaches sums of
+  // rows past M.  Fills xa for the round's super-chunks and their sums of x.
+  const auto spread = [&](const P& p, int v, typename Op::X (&xa)[SW][4], f32x4 (&xs)[NG]) {
+    wave_fence();
 #pragma unroll
-    for (int u = 0; u < SW; ++u)
+    for (int q = 0; q < MQ; ++q) {
+      const int row = 4 * q + (lane >> 4);
+      lds_x[wave][16 * row + ((lane & 15) ^ row)] = p.x[v][q];
+    }
+    wave_fence();
+    const u32x4* const xrow = &lds_x[wave][16 * nl];
+#pragma unroll
+    for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u) {
+      const int p0 = 8 * XB * (u - v * SW / XR);  // first piece of super-chunk u
+#pragma unroll
+      for (int j = 0; j < 4; j += PAIRS ? 2 : 1) {
+        if constexpr (A == Act::kBf16) {
+          xa[u][j] = xrow[(p0 + 4 * j + g) ^ nl];
+        } else if constexpr (PAIRS) {
+          const u32x4 d = xrow[(p0 + 2 * j + g) ^ nl];
+          xa[u][j] = Op::of(u32x2{d.x, d.y});
+          xa[u][j + 1] = Op::of(u32x2{d.z, d.w});
+        } else {
+          xa[u][j] = Op::of(reinterpret_cast<const u32x2*>(&xrow[(p0 + 2 * j + (g >> 1)) ^ nl])[g & 1]);
+        }
+      }
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         Acc c = {};
@@ -370,46 +460,96 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
 #pragma unroll
         for (int i = 0; i < 4; ++i) xs[u * PER + q][i] = (float)c[i];
       }
-    // Tile by tile: tile t has landed once only the SW (T - 1 - t) newer
-    // loads are outstanding (loads, LDS DMA included, complete in order), and
-    // its products overlap the later tiles' DMA.
+    }
+  };
+
+  // Scales, zero points and grouped scales of x to LDS.
+  const auto spread_scales = [&](const P& p) {
+    wave_fence();
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      __builtin_amdgcn_sched_barrier(0);
-      wait_newer<SW>(T - 1 - t);
-      __builtin_amdgcn_sched_barrier(0);
-      u32x4 cw[SW];
-#pragma unroll
-      for (int u = 0; u < SW; ++u) cw[u] = lds_c[wave][t][16 * nl + ((4 * u + g) ^ nl)];
-#pragma unroll
-      for (int u = 0; u < SW; ++u) {
-        const u32x4 d = regroup<GS>(cw[u]);
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const int at = u * PER + q;
-          Acc c = {};
-#pragma unroll
-          for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(d[j]), c);
-          const float s = __uint_as_float(at & 1 ? sw[t][at / 2] & 0xFFFF0000u : sw[t][at / 2] << 16);
-          const float z = (float)((zw[t][at / 4] >> (8 * (at & 3))) & 0xFFu);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[t][i] = __builtin_fmaf(__builtin_fmaf(-z, xs[at][i], (float)c[i]), grouped ? s * fx[at][i] : s, acc[t][i]);
-        }
+    for (int a = 0; a < P::SI; ++a) {
+      const int item = 64 * a + lane;
+      if (R * NG / 4 % 64 == 0 || item < R * NG / 4) {
+        reinterpret_cast<u32x2*>(st_s)[item] = p.s[a];
+        st_z[item] = p.z[a];
       }
     }
+    if constexpr (GX) {
+#pragma unroll
+      for (int a = 0; a < NG / 4; ++a) st_f[64 * a + lane] = p.f[a];  // [group 4 a + g][row nl]
+    }
+    wave_fence();
+  };
+
+  // Products of super-chunk u of tile t.
+  const auto multiply = [&](int t, int u, u32x4 codes, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
+    const u32x4 d = regroup<PAIRS>(codes);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int at = u * PER + q;
+      const u32x2 s4 = reinterpret_cast<const u32x2*>(st_s)[at / 4 * R + 16 * t + nl];
+      const uint32_t z4 = st_z[at / 4 * R + 16 * t + nl];
+      Acc c = {};
+#pragma unroll
+      for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(d[j]), c);
+      const uint32_t s2 = at & 2 ? s4.y : s4.x;
+      const float s = __uint_as_float(at & 1 ? s2 & 0xFFFF0000u : s2 << 16);
+      const float z = (float)((z4 >> (8 * (at & 3))) & 0xFFu);
+      f32x4 f = f32x4{s, s, s, s};
+      if constexpr (GX) f *= *reinterpret_cast<const f32x4*>(&st_f[16 * at + 4 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[t][i] = __builtin_fmaf(__builtin_fmaf(-z, xs[at][i], (float)c[i]), f[i], acc[t][i]);
+    }
+  };
+
+  const auto compute = [&](const P& p) {
+    typename Op::X xa[SW][4];
+    f32x4 xs[NG];
+    if constexpr (T == 1) {
+      // round by round: few operands are live
+      spread_scales(p);
+#pragma unroll
+      for (int v = 0; v < XR; ++v) {
+        spread(p, v, xa, xs);
+#pragma unroll
+        for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u)
+          multiply(0, u, tile(0)[16 * nl + ((4 * u + chunk_of<PAIRS>(g)) ^ nl)], xa, xs);
+      }
+    } else {
+      // tile by tile, in the order of the DMA, so that a tile's products
+      // overlap the later tiles' DMA
+#pragma unroll
+      for (int v = 0; v < XR; ++v) spread(p, v, xa, xs);
+      spread_scales(p);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 cw[SW];
+#pragma unroll
+        for (int u = 0; u < SW; ++u) cw[u] = tile(t)[16 * nl + ((4 * u + chunk_of<PAIRS>(g)) ^ nl)];
+#pragma unroll
+        for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa, xs);
+      }
+    }
+  };
+
+  for (int s0 = sbeg; s0 < send; s0 += SW) {  // wave-uniform
+    P p;
+    load(p, s0);
+    compute(p);
   }
 
-  // waves are added in wave order, through the first T KB of each one's codes
-  f32x4* const red_w = reinterpret_cast<f32x4*>(&lds_c[wave][0][0]);
+  // waves are added in wave order, through each one's first tile of codes
+  f32x4* const red_w = reinterpret_cast<f32x4*>(lds_c0[wave]);
 #pragma unroll
   for (int t = 0; t < T; ++t) red_w[64 * t + lane] = acc[t];
   __syncthreads();
   for (int idx = threadIdx.x; idx < T * 64; idx += NW * 64) {
     const int t = idx >> 6, l = idx & 63;
-    f32x4 sum = reinterpret_cast<const f32x4*>(&lds_c[0][0][0])[64 * t + l];
+    f32x4 sum = reinterpret_cast<const f32x4*>(lds_c0[0])[64 * t + l];
 #pragma unroll
-    for (int v = 1; v < NW; ++v) sum += reinterpret_cast<const f32x4*>(&lds_c[v][0][0])[64 * t + l];
+    for (int v = 1; v < NW; ++v) sum += reinterpret_cast<const f32x4*>(lds_c0[v])[64 * t + l];
     const int n = n0 + 16 * t + (l & 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -425,48 +565,68 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   }
 }
 
-#ifndef INT4_T_TALL
-#define INT4_T_TALL 4
-#define INT4_NW_TALL 8
-#define INT4_T_SHORT 1
-#define INT4_NW_SHORT 16
-#endif
+// Waves and rows per workgroup, from a sweep over N = 256..28672, K =
+// 512..14336 and M = 1..16 of the three types (us a call, back to back):
+//  * N <= 4096: 16 rows, so that up to 256 CUs have a workgroup each; 16 waves
+//    where K has more than one pass for each of 8 (4096 x 14336, bf16, M = 3:
+//    8.9 with 16, 9.7 with 8; 4096 x 4096: 5.3, 5.1);
+//  * N <= 8192: 32 rows for the same reason (8192 x 4096, INT8, M = 16: 6.4;
+//    16 rows 6.8, 64 rows 7.9);
+//  * above: 64 rows, x being read once per workgroup (14336 x 4096, INT8, M =
+//    16: 8.9; 32 rows 10.9, 16 rows 11.8).
+template <Act A, bool GX>
+hipError_t launch_mfma(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, int G, void* y, int b,
+                       hipStream_t stream) {
+  const int wide = K % 512 == 0 && (reinterpret_cast<uintptr_t>(w.scales) & 7) == 0 &&
+                   (reinterpret_cast<uintptr_t>(w.zeros) & 3) == 0;
+#define INT4_MFMA(GS, T, NW, MQ)                                                                                   \
+  hipLaunchKernelGGL((int4_gemv_mfma_kernel<A, GX, GS, T, NW, MQ>), dim3((unsigned)((N + 16 * T - 1) / (16 * T))), \
+                     dim3(NW * 64), 0, stream, x, w, (int)M, (int)N, (int)K, G, wide, y, b)
+#define INT4_ROWS(GS, T, NW)                  \
+  do {                                        \
+    if (M <= 4) INT4_MFMA(GS, T, NW, 1);      \
+    else if (M <= 8) INT4_MFMA(GS, T, NW, 2); \
+    else INT4_MFMA(GS, T, NW, 4);             \
+  } while (0)
+#define INT4_SHAPE(GS)                          \
+  do {                                          \
+    if (N > 8192) INT4_ROWS(GS, 4, 8);          \
+    else if (N > 4096) INT4_ROWS(GS, 2, 8);     \
+    else if (K > 4096) INT4_ROWS(GS, 1, 16);    \
+    else INT4_ROWS(GS, 1, 8);                   \
+  } while (0)
+  if (w.group == 128) INT4_SHAPE(128);
+  else if (w.group == 64) INT4_SHAPE(64);
+  else INT4_SHAPE(32);
+#undef INT4_SHAPE
+#undef INT4_ROWS
+#undef INT4_MFMA
+  return hipGetLastError();
+}
 
+// One row of few weights goes to the dot products, which start sooner (1024 x
+// 14336, bf16: 5.8 us, the matrix kernel 8.1; 4096 x 8192: 6.5, 7.2); a large
+// weight to the matrix kernel, which reads longer runs (4096 x 14336: 11.4,
+// 8.9; 14336 x 4096: 9.0, 8.5; 8192 x 8192: 9.9, 9.6).  K is split over 2 or 4 waves.
 template <Act A>
 hipError_t launch_gemv(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, void* y, int b,
                        hipStream_t stream) {
   const int G = (int)((K + w.group - 1) / w.group);
-  const int64_t nch = K / 32;  // 16-byte code chunks per row
-  if (M == 1 && nch <= 1024) {
+  if (M == 1 && K <= 16384 && (N <= 2048 || (N <= 4096 && K <= 8192))) {
     const int shift = w.group == 32 ? 0 : w.group == 64 ? 1 : 2;  // chunk -> scale group
-#define INT4_M1(CH, RW, S)                                                                                      \
+#define INT4_M1(CH, RW, S)                                                                                           \
   hipLaunchKernelGGL((int4_gemv_m1_kernel<A, CH, RW, S>), dim3((unsigned)((N + (4 / S) * RW - 1) / ((4 / S) * RW))), \
                      dim3(256), 0, stream, x, w, shift, (int)N, (int)K, G, y, b)
-    if (nch <= 128) INT4_M1(1, 4, 2);         // K <= 4096
-    else if (nch <= 256) INT4_M1(2, 4, 2);    // K <= 8192
-    else if (nch <= 512) INT4_M1(4, 4, 2);    // K <= 16384
-    else INT4_M1(4, 4, 4);                    // K <= 32768
+    if (K <= 4096) INT4_M1(1, 2, 2);       // CH S 64 chunks of 32
+    else if (K <= 8192) INT4_M1(1, 2, 4);
+    else INT4_M1(2, 2, 4);
 #undef INT4_M1
     return hipGetLastError();
   }
-  const int wide = K % 512 == 0 && (reinterpret_cast<uintptr_t>(w.scales) & 7) == 0 &&
-                   (reinterpret_cast<uintptr_t>(w.zeros) & 3) == 0;
-#define INT4_MFMA(GS, T, NW)                                                                                     \
-  hipLaunchKernelGGL((int4_gemv_mfma_kernel<A, GS, T, NW>), dim3((unsigned)((N + 16 * T - 1) / (16 * T))), dim3(NW * 64), \
-                     0, stream, x, w, (int)M, (int)N, (int)K, G, wide, y, b)
-#define INT4_SHAPE(GS)                                           \
-  if (N >= 8192) INT4_MFMA(GS, INT4_T_TALL, INT4_NW_TALL);       \
-  else INT4_MFMA(GS, INT4_T_SHORT, (GS == 128 ? INT4_NW_SHORT : 8))
-  if (w.group == 128) {
-    INT4_SHAPE(128);
-  } else if (w.group == 64) {
-    INT4_SHAPE(64);
-  } else {
-    INT4_SHAPE(32);
+  if constexpr (A != Act::kBf16) {
+    if (x.grouped) return launch_mfma<A, true>(x, w, M, N, K, G, y, b, stream);
   }
-#undef INT4_SHAPE
-#undef INT4_MFMA
-  return hipGetLastError();
+  return launch_mfma<A, false>(x, w, M, N, K, G, y, b, stream);
 }
 
 hipError_t launch_int4_gemv(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, void* y,

@@ -49,6 +49,12 @@ def lib():
     return _lib
 
 
+# A decode call costs the host about as much as the GPU, so what every call
+# does is kept short: torch's own handle of the current stream, and checks by
+# attribute without helper objects.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -60,27 +66,35 @@ def _code(table, dtype, what):
     return code
 
 
-def _enter(*ts):
-    """Checks that the tensors are on the current device; its stream's handle."""
-    dev = torch.cuda.current_device()
-    for t in ts:
+def _stream(first, *others):
+    """The current stream of the current device, on which all the tensors have to be.
+
+    (A stream that is being captured is refused by the library, before it
+    launches anything.)"""
+    dev = first.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current GPU; got one on {first.device}")
+    for t in others:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current GPU (cuda:{dev}); got one on {t.device}")
-    if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("int4 calls are not graph-capture safe: the current stream is being captured")
-    return torch.cuda.current_stream(dev).cuda_stream
+            raise ValueError(f"tensors must be on the current GPU; got one on {t.device}")
+    return _raw_stream(dev)
 
 
-def _contiguous(*ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+def _done(fn, status):
+    if status:
+        _nv._check(fn, status)
+
+
+def _contiguous(t):
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
 
 
 def _matrix(t, what):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be a 2-D tensor")
-    return t.shape
+    return shape
 
 
 def _given(out, shape, dtype, what="out"):
@@ -96,16 +110,18 @@ def _groups(cols, group_size):
 
 
 def _check_weight(codes, scales, zeros, group_size):
-    """(N, K) of a packed weight, whose shapes and types have to agree."""
+    """(N, K, G) of a packed weight, whose shapes and types have to agree."""
     N, half = _matrix(codes, "codes")
-    G = _groups(2 * half, group_size)
-    if codes.dtype != torch.uint8 or scales.dtype != torch.bfloat16 or (zeros is not None and zeros.dtype != torch.uint8):
-        raise ValueError("a packed weight is uint8 codes [N, K/2], bfloat16 scales [N, G] and uint8 zeros [N, G] or None")
-    if scales.shape != (N, G) or (zeros is not None and zeros.shape != (N, G)):
-        raise ValueError(f"scales {tuple(scales.shape)} and zeros {None if zeros is None else tuple(zeros.shape)} do not "
-                         f"match codes {tuple(codes.shape)} in groups of {group_size}: expected {(N, G)}")
-    _contiguous(codes, scales, zeros)
-    return N, 2 * half
+    want = (N, _groups(2 * half, group_size))
+    if (codes.dtype != torch.uint8 or scales.dtype != torch.bfloat16 or scales.shape != want
+            or (zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != want))):
+        raise ValueError(f"a packed weight is uint8 codes [N, K/2], bfloat16 scales [N, G] and uint8 zeros [N, G] or None, "
+                         f"G = {want[1]} for groups of {group_size}; got codes {codes.dtype} {tuple(codes.shape)}, scales "
+                         f"{scales.dtype} {tuple(scales.shape)}"
+                         + ("" if zeros is None else f", zeros {zeros.dtype} {tuple(zeros.shape)}"))
+    if not (codes.is_contiguous() and scales.is_contiguous() and (zeros is None or zeros.is_contiguous())):
+        raise ValueError("tensors must be contiguous")
+    return N, 2 * half, want[1]
 
 
 def quantize(w, group_size=128, symmetric=False, out=None):
@@ -119,7 +135,7 @@ def quantize(w, group_size=128, symmetric=False, out=None):
     G = _groups(K, group_size)
     _contiguous(w)
     if out is None:
-        stream = _enter(w)
+        stream = _stream(w)
         codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
         scales = torch.empty((N, G), dtype=torch.bfloat16, device=w.device)
         zeros = None if symmetric else torch.empty((N, G), dtype=torch.uint8, device=w.device)
@@ -131,48 +147,48 @@ def quantize(w, group_size=128, symmetric=False, out=None):
         _given(scales, (N, G), torch.bfloat16, "out's scales")
         if zeros is not None:
             _given(zeros, (N, G), torch.uint8, "out's zeros")
-        stream = _enter(w, codes, scales, zeros)
-    _nv._check("int4_quantize", lib().int4_quantize(_ptr(w), dt, N, K, group_size, _ptr(codes), _ptr(scales),
-                                                    _ptr(zeros), stream))
+        stream = _stream(w, codes, scales, zeros)
+    _done("int4_quantize", lib().int4_quantize(w.data_ptr(), dt, N, K, group_size, codes.data_ptr(), scales.data_ptr(),
+                                               _ptr(zeros), stream))
     return codes, scales, zeros
 
 
 def dequant(codes, scales, zeros=None, group_size=128, out_dtype=torch.float32, out=None):
     """scale * (code - zero) as a [N, K] fp32 (exact) or bf16 tensor."""
-    N, K = _check_weight(codes, scales, zeros, group_size)
+    N, K, _ = _check_weight(codes, scales, zeros, group_size)
     if out is None:
         dt = _code(_FLOATS, out_dtype, "output")
-        stream = _enter(codes, scales, zeros)
+        stream = _stream(codes, scales, zeros)
         out = torch.empty((N, K), dtype=out_dtype, device=codes.device)
     else:
         dt = _code(_FLOATS, out.dtype, "output")
         _given(out, (N, K), out.dtype)
-        stream = _enter(codes, scales, zeros, out)
-    _nv._check("int4_dequant", lib().int4_dequant(_ptr(codes), _ptr(scales), _ptr(zeros), N, K, group_size, _ptr(out),
-                                                  dt, stream))
+        stream = _stream(codes, scales, zeros, out)
+    _done("int4_dequant", lib().int4_dequant(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group_size,
+                                             out.data_ptr(), dt, stream))
     return out
 
 
 def _product(x, codes, scales, zeros, group_size, out_dtype, out, x_scales=None):
     """Shape checks and output of a decode product: (M, N, K, out, its dtype code, stream)."""
-    N, K = _check_weight(codes, scales, zeros, group_size)
+    N, K, G = _check_weight(codes, scales, zeros, group_size)
     M, Kx = _matrix(x, "x")
     if Kx != K:
         raise ValueError(f"x has {Kx} columns, the weight {K}")
     if x_scales is not None:
-        G = scales.shape[1]
         if x_scales.dtype != torch.float32 or (x_scales.shape != (M, 1) and x_scales.shape != (M, G)):
             raise ValueError(f"x_scales must be a float32 tensor of shape {(M, 1)} or {(M, G)}; got {x_scales.dtype} "
                              f"{tuple(x_scales.shape)}")
-    _contiguous(x, x_scales)
+        _contiguous(x_scales)
+    _contiguous(x)
     if out is None:
         dt = _code(_FLOATS, out_dtype, "output")
-        stream = _enter(x, codes, scales, zeros, x_scales)
+        stream = _stream(x, codes, scales, zeros, x_scales)
         out = torch.empty((M, N), dtype=out_dtype, device=x.device)
     else:
         dt = _code(_FLOATS, out.dtype, "output")
         _given(out, (M, N), out.dtype)
-        stream = _enter(x, codes, scales, zeros, x_scales, out)
+        stream = _stream(x, codes, scales, zeros, x_scales, out)
     return M, N, K, out, dt, stream
 
 
@@ -181,8 +197,8 @@ def gemv_w4a16(x, codes, scales, zeros=None, group_size=128, out_dtype=torch.bfl
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bfloat16 tensor")
     M, N, K, out, dt, stream = _product(x, codes, scales, zeros, group_size, out_dtype, out)
-    _nv._check("int4_gemv_w4a16", lib().int4_gemv_w4a16(_ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), group_size,
-                                                        M, N, K, _ptr(out), dt, stream))
+    _done("int4_gemv_w4a16", lib().int4_gemv_w4a16(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
+                                                   group_size, M, N, K, out.data_ptr(), dt, stream))
     return out
 
 
@@ -194,10 +210,10 @@ def gemv_w4a8(x, x_scales, codes, scales, zeros=None, group_size=128, out_dtype=
     the same."""
     xt = _code(_BYTES, x.dtype, "activation")
     M, N, K, out, dt, stream = _product(x, codes, scales, zeros, group_size, out_dtype, out, x_scales)
-    _nv._check("int4_gemv_w4a8", lib().int4_gemv_w4a8(_ptr(x), xt, _ptr(x_scales),
-                                                      0 if x_scales.shape[1] == 1 else group_size, _ptr(codes),
-                                                      _ptr(scales), _ptr(zeros), group_size, M, N, K, _ptr(out), dt,
-                                                      stream))
+    _done("int4_gemv_w4a8", lib().int4_gemv_w4a8(x.data_ptr(), xt, x_scales.data_ptr(),
+                                                 0 if x_scales.shape[1] == 1 else group_size, codes.data_ptr(),
+                                                 scales.data_ptr(), _ptr(zeros), group_size, M, N, K, out.data_ptr(), dt,
+                                                 stream))
     return out
 
 
@@ -220,7 +236,7 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
     x itself where type and layout agree (the sum in place)."""
     M, K = _matrix(x, "x")
     xt, qt = _code(_FLOATS, x.dtype, "x"), _code(_BYTES, out_dtype if out is None else out[0].dtype, "output")
-    if not (eps >= 0 and math.isfinite(eps)):
+    if not 0 <= eps < math.inf:
         raise ValueError(f"eps={eps}: expected a finite value >= 0")
     G = _groups(K, group_size) if group_size else 1
     xs, rt, rs, wt = _row_stride(x, "x"), F32, 0, F32
@@ -233,7 +249,7 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
         if weight.shape != (K,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous tensor of shape {(K,)}")
     if out is None:
-        stream = _enter(x, weight, residual)
+        stream = _stream(x, weight, residual)
         codes = torch.empty((M, K), dtype=out_dtype, device=x.device)
         scales = torch.empty((M, G), dtype=torch.float32, device=x.device)
         h = None if residual is None else torch.empty((M, K), dtype=residual.dtype, device=x.device)
@@ -245,8 +261,8 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
         _given(scales, (M, G), torch.float32, "out's scales")
         if h is not None:
             _given(h, (M, K), residual.dtype, "out's sum")
-        stream = _enter(x, weight, residual, codes, scales, h)
-    _nv._check("int4_rmsnorm_quant8",
-               lib().int4_rmsnorm_quant8(_ptr(x), xt, xs, _ptr(residual), rt, rs, _ptr(weight), wt, float(eps), M, K,
-                                         group_size, qt, _ptr(codes), _ptr(scales), _ptr(h), stream))
+        stream = _stream(x, weight, residual, codes, scales, h)
+    _done("int4_rmsnorm_quant8",
+          lib().int4_rmsnorm_quant8(x.data_ptr(), xt, xs, _ptr(residual), rt, rs, _ptr(weight), wt, eps, M, K, group_size,
+                                    qt, codes.data_ptr(), scales.data_ptr(), _ptr(h), stream))
     return codes, scales, h

@@ -434,9 +434,9 @@ def test_refusals():
     p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
     with torch.cuda.graph(g, stream=side):
         marker.add_(1.0)                             # one node, so the graph is not empty; it is never replayed
-        with pytest.raises(RuntimeError, match="not graph-capture safe"):
+        with pytest.raises(nv.NVFP4Error, match="not capture-safe"):
             int4.gemv_w4a16(x[:1], *w, group_size=32, out=y)
-        with pytest.raises(RuntimeError, match="not graph-capture safe"):
+        with pytest.raises(nv.NVFP4Error, match="not capture-safe"):
             int4.rmsnorm_quant8(x)
         st = int4.lib().int4_gemv_w4a16(p(x), p(w[0]), p(w[1]), p(w[2]), 32, 1, 8, 64, p(y), int4.F32,
                                         ctypes.c_void_p(side.cuda_stream))
