@@ -10,23 +10,27 @@
 
 namespace nvfp4 {
 
-constexpr int kRuns = 4;  // runs of 64 vectors a wave keeps in flight
+// Runs of 64 vectors that a wave keeps in flight.  (us, 14336 x 4096: fp32
+// quantize 50.1, 50.2, 51.2 with 1, 2, 4; bf16 38.5, 32.6, 31.8; dequant to
+// bf16 39.9, 33.9, 32.7; to fp32, whose stores are twice as wide, 57.9, 57.2,
+// 76.2.  1024 x 4096 bf16 quantize 4.7, 4.4, 5.1.)
+constexpr int kQuantizeRuns = 2, kDequantRunsBf16 = 4, kDequantRunsF32 = 2;
 
 // The rows a launch sees: the tensor's own, or one of all its elements.
 struct RowView {
   int64_t rows, n8, padded8;  // vectors of a row, and that rounded up to whole groups
   int64_t runs;               // runs of 64 vectors of a row
-  int64_t units;              // kRuns runs of a row each
+  int64_t units;              // as many runs of a row as a wave keeps in flight, each
 };
 
-static RowView row_view(int64_t rows, int64_t cols, int group) {
+static RowView row_view(int64_t rows, int64_t cols, int group, int runs) {
   RowView v;
   const bool flat = cols % group == 0;
   v.rows = flat ? 1 : rows;
   v.n8 = (flat ? rows * cols : cols) / 8;
   v.padded8 = (v.n8 + group / 8 - 1) / (group / 8) * (group / 8);
   v.runs = (v.padded8 + 63) / 64;
-  v.units = (v.runs + kRuns - 1) / kRuns;
+  v.units = (v.runs + runs - 1) / runs;
   return v;
 }
 
@@ -48,14 +52,29 @@ struct Raw {
   }
 };
 
-// rne(w / s) for |w / s| < 16, given t = w * inv with inv within 2 ulp of
-// 1 / s: t is off by less than 2^-18, so only a t that near to half way
-// between integers needs the exact quotient (fp64: w has 24 significant bits
-// and s 8, so a quotient that is not half way is further from it than fp64
-// rounds).
+// rne(w / s) for |w / s| < 16 and s >= 2^-100 (8 significant bits), with inv
+// the hardware's estimate of 1 / s.
+//  * bf16 w: a quotient of two 8-bit numbers is half way between integers or
+//    further from it than 2^-13, and one corrected step gives it to within an
+//    ulp, exactly where it has few bits, as half way does.
+//  * fp32 w: t = w inv is off by less than 2^-18; only where that may decide
+//    is w compared with the border itself, (k + 1/2) s for k = floor(t), which
+//    has 13 bits and is exact (a floor that is one too low next to an integer
+//    does not matter).
+__device__ __forceinline__ float quotient_bf16(float w, float s, float inv) {
+  const float q = w * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, s, w), inv, q);
+}
 constexpr float kHalfway = 0.4999f;
 
-template <bool BF16>
+__device__ __forceinline__ float nearest_f32(float w, float s, float t) {
+  const float k = __builtin_floorf(t), border = (k + 0.5f) * s;
+  const float even = __builtin_rintf(k + 0.5f);
+  const float down = w < border ? k : even;
+  return w > border ? k + 1.0f : down;
+}
+
+template <bool BF16, int RUNS>
 __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restrict__ x, RowView rv, int L, int64_t G,
                                                             uint8_t* __restrict__ codes,
                                                             uint16_t* __restrict__ scales,
@@ -65,15 +84,15 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
   for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
        u += (int64_t)gridDim.x * 4) {
     const int64_t row = rv.rows == 1 ? 0 : u / rv.units;
-    const int64_t v0 = (u - row * rv.units) * kRuns * 64 + lane;
-    Raw<BF16> raw[kRuns];
+    const int64_t v0 = (u - row * rv.units) * RUNS * 64 + lane;
+    Raw<BF16> raw[RUNS];
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
+    for (int k = 0; k < RUNS; ++k) {
       if (v0 + 64 * k < rv.n8) raw[k].load(x, row * rv.n8 + v0 + 64 * k);
       else raw[k].zero();
     }
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
+    for (int k = 0; k < RUNS; ++k) {
       const int64_t v = v0 + 64 * k;
       float lo = 0.0f, hi = 0.0f, w[8];
 #pragma unroll
@@ -88,16 +107,30 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
       const uint32_t sb = f32_to_bf16_bits((float)range);
       const float s = bf16_bits_to_f32(sb);
       const float inv = __builtin_amdgcn_rcpf(s);
-      const bool odd_scale = s < 0x1p-126f;  // 0 or below the normal range: the estimate does not hold
-      float t[9];                            // the eight quotients, and the zero point's
-      bool near = odd_scale;
+      const bool odd_scale = s < 0x1p-100f;  // also 0
+      float t[9];                            // the eight codes before the zero point, and that
+      if constexpr (BF16) {
 #pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const float q = (j < 8 ? w[j] : -lo) * inv;
-        t[j] = __builtin_rintf(q);
-        near |= fabsf(q - t[j]) > kHalfway;
+        for (int j = 0; j < 9; ++j) t[j] = __builtin_rintf(quotient_bf16(j < 8 ? w[j] : -lo, s, inv));
+      } else {
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          const float q = (j < 8 ? w[j] : -lo) * inv;
+          t[j] = __builtin_rintf(q);
+          near |= fabsf(q - t[j]) > kHalfway;
+        }
+        if (near) {
+#pragma unroll
+          for (int j = 0; j < 9; ++j) {
+            const float v = j < 8 ? w[j] : -lo;
+            t[j] = nearest_f32(v, s, v * inv);
+          }
+        }
       }
-      if (near) {
+      if (odd_scale) {
+        // fp64: w has 24 significant bits and s 8, so a quotient that is not
+        // half way is further from it than fp64 rounds
 #pragma unroll
         for (int j = 0; j < 9; ++j)
           t[j] = s == 0.0f ? 0.0f : (float)__builtin_rint((double)(j < 8 ? w[j] : -lo) / (double)s);
@@ -122,7 +155,7 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
   }
 }
 
-template <bool BF16>
+template <bool BF16, int RUNS>
 __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __restrict__ codes,
                                                            const uint16_t* __restrict__ scales,
                                                            const uint8_t* __restrict__ zeros, RowView rv, int L,
@@ -132,10 +165,10 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
   for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
        u += (int64_t)gridDim.x * 4) {
     const int64_t row = rv.rows == 1 ? 0 : u / rv.units;
-    const int64_t v0 = (u - row * rv.units) * kRuns * 64 + lane;
-    uint32_t w[kRuns], sb[kRuns], z[kRuns];
+    const int64_t v0 = (u - row * rv.units) * RUNS * 64 + lane;
+    uint32_t w[RUNS], sb[RUNS], z[RUNS];
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
+    for (int k = 0; k < RUNS; ++k) {
       const int64_t v = min(v0 + 64 * k, rv.n8 - 1);
       const int64_t slot = row * G + v / L;
       w[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes) + row * rv.n8 + v);
@@ -143,7 +176,7 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
       z[k] = zeros ? zeros[slot] : 8u;
     }
 #pragma unroll
-    for (int k = 0; k < kRuns; ++k) {
+    for (int k = 0; k < RUNS; ++k) {
       const int64_t v = v0 + 64 * k;
       const float s = bf16_bits_to_f32(sb[k]), zf = (float)z[k];
       const uint32_t lo = w[k] & 0x0F0F0F0Fu, hi = (w[k] >> 4) & 0x0F0F0F0Fu;
@@ -172,25 +205,26 @@ static dim3 stream_grid(const RowView& v) {
 
 hipError_t launch_int4_quantize(const void* x, bool bf16, int64_t rows, int64_t cols, int group, uint8_t* codes,
                                 uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const RowView v = row_view(rows, cols, group);
+  const RowView v = row_view(rows, cols, group, kQuantizeRuns);
   const int64_t G = (cols + group - 1) / group;
-#define INT4_QUANTIZE(B) \
-  hipLaunchKernelGGL(int4_quantize_kernel<B>, stream_grid(v), dim3(256), 0, stream, x, v, group / 8, G, codes, scales, zeros)
-  if (bf16) INT4_QUANTIZE(true);
-  else INT4_QUANTIZE(false);
+#define INT4_QUANTIZE(B, R)                                                                                        \
+  hipLaunchKernelGGL((int4_quantize_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, x, v, group / 8, G, codes, \
+                     scales, zeros)
+  if (bf16) INT4_QUANTIZE(true, kQuantizeRuns);
+  else INT4_QUANTIZE(false, kQuantizeRuns);
 #undef INT4_QUANTIZE
   return hipGetLastError();
 }
 
 hipError_t launch_int4_dequant(const Int4Weight& w, int64_t rows, int64_t cols, void* out, bool bf16_out,
                                hipStream_t stream) {
-  const RowView v = row_view(rows, cols, w.group);
+  const RowView v = row_view(rows, cols, w.group, bf16_out ? kDequantRunsBf16 : kDequantRunsF32);
   const int64_t G = (cols + w.group - 1) / w.group;
-#define INT4_DEQUANT(B)                                                                                       \
-  hipLaunchKernelGGL(int4_dequant_kernel<B>, stream_grid(v), dim3(256), 0, stream, w.codes, w.scales, w.zeros, v, \
+#define INT4_DEQUANT(B, R)                                                                                             \
+  hipLaunchKernelGGL((int4_dequant_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, w.codes, w.scales, w.zeros, v, \
                      w.group / 8, G, out)
-  if (bf16_out) INT4_DEQUANT(true);
-  else INT4_DEQUANT(false);
+  if (bf16_out) INT4_DEQUANT(true, kDequantRunsBf16);
+  else INT4_DEQUANT(false, kDequantRunsF32);
 #undef INT4_DEQUANT
   return hipGetLastError();
 }

@@ -9,8 +9,12 @@
 // columns are 4, 8 and 16 neighbouring lanes.
 //
 // A code is the nearest to the exact y / s, so sums, products and quotients
-// are fp64: the fp64 pipe runs at the fp32 rate on this chip, and the dozen
-// operations an element takes fit under the 7 bytes it moves.
+// are fp64 wherever fp32 would round: h^2 always, the rest where h or w is
+// fp32.  With bf16 h and w the products h w are exact in fp32, and y / s in
+// fp32 decides a code unless it is within its error of half way between two
+// codes; only a wave that has such an element redoes its vectors in fp64.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
 #include "lanes.hpp"
@@ -74,20 +78,14 @@ struct Vec8 {
   }
 };
 
-__device__ __forceinline__ void load_weight(const NormArgs& a, int i, float w[8]) {
-  if (!a.weight) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-  } else if (a.w_bf16) {
-    Vec8<true> v;
-    v.load(a.weight, i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = v.at(j);
-  } else {
-    Vec8<false> v;
-    v.load(a.weight, i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = v.at(j);
+template <bool WBF>
+__device__ __forceinline__ void load_weight(const NormArgs& a, int i, Vec8<WBF>& w) {
+  if (a.weight) {
+    w.load(a.weight, i);
+  } else {  // ones
+    const uint32_t one = WBF ? 0x3F803F80u : 0x3F800000u;
+    w.a[0] = u32x4{one, one, one, one};
+    w.a[WBF ? 0 : 1] = w.a[0];
   }
 }
 
@@ -122,87 +120,118 @@ __device__ __forceinline__ u32x2 encode_e4m3(const double p[8], double k) {
   return q;
 }
 
-template <int T, int V, bool XBF, Res RES>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_quant_kernel(NormArgs a, double inv_cols, double inv_top) {
+// INT8 codes from exact fp32 products p and k rounded to fp32: u = p k is off
+// by less than 2^-22 |u| < 2^-15; `near` where that may decide a code.  (For
+// E4M3 the test for half way costs more than it saves.)
+__device__ __forceinline__ u32x2 encode_i8_fast(const float p[8], float k, bool& near) {
+  uint32_t b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float u = p[j] * k;
+    const float m = u + 12582912.0f;  // 1.5 2^23: the low byte is the code
+    near |= fabsf(u - (m - 12582912.0f)) > 0.49996f;
+    b[j] = __float_as_uint(m);
+  }
+  u32x2 q;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const uint32_t lo = __builtin_amdgcn_perm(b[4 * d + 1], b[4 * d], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[4 * d + 3], b[4 * d + 2], 0x04000c0cu);
+    q[d] = lo | hi;
+  }
+  return q;
+}
+// A value the compiler takes for a new one, so that what is computed from it
+// is not kept from earlier.
+__device__ __forceinline__ float fresh(float v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+template <int T, int V, bool XBF, Res RES, bool WBF>
+__global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1) void rmsnorm_quant_kernel(NormArgs a, double inv_cols, double inv_top) {
   constexpr int B = T < 256 ? 256 : T, TEAMS = B / T, NW = T / 64;
-  __shared__ double red[2][16];
   const int t = threadIdx.x % T;
   const int64_t r = (int64_t)blockIdx.x * TEAMS + threadIdx.x / T;
   const int n8 = a.cols / 8;
   const bool live_row = r < a.rows;
-  // The weight is read again for the codes where a thread has many vectors
-  // (an L1 or L2 hit; the registers are worth more).
-  constexpr bool kKeep = V <= 2;
+  // Where a thread has many vectors the weight, and then h too, is read again
+  // for the codes (a cache hit; the registers are worth more: two workgroups
+  // of 1024 threads a CU instead of one take 2000 x 14336 from 50 to 43 us).
+  constexpr bool kKeep = V <= (T == 1024 ? 1 : 2), kKeepH = V <= 4;
   constexpr bool HBF = RES == Res::kNone ? XBF : RES == Res::kBf16;
-  Vec8<HBF> h[V];
-  float w[kKeep ? V : 1][8];
-  double ss = 0.0, m[V];
+  constexpr bool kFast = HBF && WBF;
+  using Max = typename std::conditional<kFast, float, double>::type;
+  Vec8<HBF> h[kKeepH ? V : 1];
+  Vec8<WBF> w[kKeep ? V : 1];
+  double ss = 0.0;
+  Max m[V];
+  __shared__ double red_ss[16];
+  __shared__ Max red_max[16];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = t + T * v;
-    float* const wv = w[kKeep ? v : 0];
-    h[v].zero();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wv[j] = 0.0f;
+    Vec8<WBF>& wv = w[kKeep ? v : 0];
+    Vec8<HBF>& hv = h[kKeepH ? v : 0];
+    hv.zero();
+    wv.zero();
     if (live_row && i < n8) {
       if constexpr (RES == Res::kNone) {
-        h[v].load(a.x, r * a.x_stride + 8 * i);
+        hv.load(a.x, r * a.x_stride + 8 * i);
       } else {
         Vec8<XBF> x;
         x.load(a.x, r * a.x_stride + 8 * i);
-        h[v].load(a.residual, r * a.res_stride + 8 * i);
+        hv.load(a.residual, r * a.res_stride + 8 * i);
         float sum[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = x.at(j) + h[v].at(j);
-        h[v].set(sum);
-        h[v].store(a.residual_out, r * a.cols + 8 * i);
+        for (int j = 0; j < 8; ++j) sum[j] = x.at(j) + hv.at(j);
+        hv.set(sum);
+        hv.store(a.residual_out, r * a.cols + 8 * i);
       }
-      load_weight(a, 8 * i, wv);
+      load_weight<WBF>(a, 8 * i, wv);
     }
-    m[v] = 0.0;
+    m[v] = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const double d = (double)h[v].at(j);
+      const double d = (double)hv.at(j);
       ss = __builtin_fma(d, d, ss);
-      m[v] = fmax(m[v], fabs(d * (double)wv[j]));
+      if constexpr (kFast) m[v] = fmaxf(m[v], fabsf(hv.at(j) * wv.at(j)));
+      else m[v] = fmax(m[v], fabs(d * (double)wv.at(j)));
     }
+    if (V > 2) __builtin_amdgcn_sched_barrier(0);  // one vector's operands at a time
   }
   const auto add = [](double p, double q) { return p + q; };
-  const auto most = [](double p, double q) { return fmax(p, q); };
-  double all = 0.0;  // the row's maximum
+  const auto most = [](Max p, Max q) { return p > q ? p : q; };
+  Max all = 0;  // the row's maximum
   if (a.group == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) all = fmax(all, m[v]);
+    for (int v = 0; v < V; ++v) all = most(all, m[v]);
   }
-  if (T == 16) {
-    ss = lanes_all<16>(ss, add);
-    if (a.group == 0) all = lanes_all<16>(all, most);
-  } else {
-    ss = lanes_all<64>(ss, add);
-    if (a.group == 0) all = lanes_all<64>(all, most);
-  }
+  constexpr int W = T < 64 ? T : 64;
+  ss = lanes_all<W>(ss, add);
+  if (a.group == 0) all = lanes_all<W>(all, most);
   if (T > 64) {
     // 4 (16) waves: every lane reads the partial results, which the lanes of
     // a quad (of a run of 16) then combine in the same way everywhere
     const int wave = threadIdx.x / 64;
     if (threadIdx.x % 64 == 0) {
-      red[0][wave] = ss;
-      red[1][wave] = all;
+      red_ss[wave] = ss;
+      red_max[wave] = all;
     }
     __syncthreads();
-    ss = red[0][threadIdx.x % NW];
+    ss = red_ss[threadIdx.x % NW];
     ss = NW == 4 ? lanes_all<4>(ss, add) : lanes_all<16>(ss, add);
     if (a.group == 0) {
-      all = red[1][threadIdx.x % NW];
+      all = red_max[threadIdx.x % NW];
       all = NW == 4 ? lanes_all<4>(all, most) : lanes_all<16>(all, most);
     }
   }
   const double ms = __builtin_fma(ss, inv_cols, a.eps);
   const double inv = ms > 0.0 ? rsqrt64(ms) : 0.0;
   const int L = a.group / 8, G = a.group ? (a.cols + a.group - 1) / a.group : 1;
-  // scale, and the factor that turns h w into y / s (0 where all is 0)
-  const auto scale_of = [&](double top, float& s) {
-    s = (float)(top * inv * inv_top);
+  // scale, and the factor that turns h w into y / s
+  const auto scale_of = [&](Max top, float& s) {
+    s = (float)((double)top * inv * inv_top);
     if (s == 0.0f) s = 1.0f;
     return inv * rcp64((double)s);
   };
@@ -215,53 +244,89 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_quant_kernel(NormAr
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = t + T * v;
+    Max top = all;
+    float s = s_row;
     if (a.group) {
-      float s;
-      k = scale_of(lanes_all(m[v], L, most), s);
+      top = lanes_all(m[v], L, most);
+      k = scale_of(top, s);
       if (live_row && i < n8 && (i & (L - 1)) == 0) a.scales[r * G + i / L] = s;
     }
     if (live_row && i < n8) {
-      float* const wv = w[kKeep ? v : 0];
-      if (!kKeep) load_weight(a, 8 * i, wv);
-      double p[8];
+      Vec8<WBF>& wv = w[kKeep ? v : 0];
+      if (!kKeep) load_weight<WBF>(a, 8 * i, wv);
+      Vec8<HBF>& hv = h[kKeepH ? v : 0];
+      if constexpr (!kKeepH) {
+        if constexpr (RES == Res::kNone) hv.load(a.x, r * a.x_stride + 8 * i);
+        else hv.load(a.residual_out, r * a.cols + 8 * i);
+      }
+      u32x2 q;
+      bool exact = true;
+      if constexpr (kFast) {
+        // Where fp32 products serve: the maximum far from overflow, and so far
+        // above fp32's smallest that products which lose bits there have code
+        // 0 either way; s normal, so |u| stays below Q and half a step.
+        exact = !(top >= 0x1p-100f && top <= 0x1p126f && s >= 0x1p-120f);
+        float p[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = (double)h[v].at(j) * (double)wv[j];
-      const u32x2 q = a.e4m3 ? encode_e4m3(p, k) : encode_i8(p, k);
+        for (int j = 0; j < 8; ++j) p[j] = hv.at(j) * wv.at(j);
+        if (a.e4m3) {
+          double d[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = (double)p[j];
+          q = encode_e4m3(d, k);
+        } else {
+          q = encode_i8_fast(p, (float)k, exact);
+        }
+      }
+      if (exact) {
+        double p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          p[j] = kFast ? (double)fresh(hv.at(j)) * (double)fresh(wv.at(j)) : (double)hv.at(j) * (double)wv.at(j);
+        q = a.e4m3 ? encode_e4m3(p, k) : encode_i8(p, k);
+      }
       *reinterpret_cast<u32x2*>(reinterpret_cast<uint8_t*>(a.codes) + r * a.cols + 8 * i) = q;
     }
+    if (V > 2) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-template <bool XBF, Res RES>
+// Threads a row and vectors a thread, by the row's length, from a sweep over
+// both: the fewest vectors a thread without teams that are mostly idle.  (us:
+// 4096 x 4096, 256 x 2 25.4, 1024 x 1 28.1, 256 x 4 28.5; 2048 x 8192, 1024 x 1
+// 26.7, 256 x 4 30.5; 16384 x 1024, 64 x 2 25.4, 256 x 1 30.8.)
+template <bool XBF, Res RES, bool WBF>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int n8 = a.cols / 8;
   const double ic = 1.0 / a.cols, it = a.e4m3 ? 1.0 / 448.0 : 1.0 / 127.0;
-#define NORM_CASE(T, V)                                                                                                \
-  hipLaunchKernelGGL((rmsnorm_quant_kernel<T, V, XBF, RES>),                                                            \
-                     dim3((unsigned)((a.rows + (T < 256 ? 256 / T : 1) - 1) / (T < 256 ? 256 / T : 1))),               \
+#define NORM_CASE(T, V)                                                                                  \
+  hipLaunchKernelGGL((rmsnorm_quant_kernel<T, V, XBF, RES, WBF>),                                        \
+                     dim3((unsigned)((a.rows + (T < 256 ? 256 / T : 1) - 1) / (T < 256 ? 256 / T : 1))), \
                      dim3(T < 256 ? 256 : T), 0, stream, a, ic, it)
   if (n8 <= 16) NORM_CASE(16, 1);
   else if (n8 <= 64) NORM_CASE(64, 1);
+  else if (n8 <= 128) NORM_CASE(64, 2);
   else if (n8 <= 256) NORM_CASE(256, 1);
-  else if (a.rows <= 256 || n8 > 2048) {
-    // few rows: short loops in wide teams; also rows too long for 256 threads
-    if (n8 <= 1024) NORM_CASE(1024, 1);
-    else if (n8 <= 2048) NORM_CASE(1024, 2);
-    else if (n8 <= 4096) NORM_CASE(1024, 4);
-    else NORM_CASE(1024, 8);
-  } else {
-    if (n8 <= 512) NORM_CASE(256, 2);
-    else if (n8 <= 1024) NORM_CASE(256, 4);
-    else NORM_CASE(256, 8);
-  }
+  else if (n8 <= 512) NORM_CASE(256, 2);
+  else if (n8 <= 1024) NORM_CASE(1024, 1);
+  else if (n8 <= 2048) NORM_CASE(1024, 2);
+  else if (n8 <= 4096) NORM_CASE(1024, 4);
+  else NORM_CASE(1024, 8);
 #undef NORM_CASE
   return hipGetLastError();
 }
 
+template <bool XBF, Res RES>
+hipError_t launch_norm_w(const NormArgs& a, hipStream_t stream) {
+  // no weight counts as bf16 (ones)
+  return !a.weight || a.w_bf16 ? launch_norm<XBF, RES, true>(a, stream) : launch_norm<XBF, RES, false>(a, stream);
+}
+
 hipError_t launch_rmsnorm_quant8(const NormArgs& a, hipStream_t stream) {
-  if (!a.residual) return a.x_bf16 ? launch_norm<true, Res::kNone>(a, stream) : launch_norm<false, Res::kNone>(a, stream);
-  if (a.res_bf16) return launch_norm<true, Res::kBf16>(a, stream);
-  return a.x_bf16 ? launch_norm<true, Res::kF32>(a, stream) : launch_norm<false, Res::kF32>(a, stream);
+  if (!a.residual)
+    return a.x_bf16 ? launch_norm_w<true, Res::kNone>(a, stream) : launch_norm_w<false, Res::kNone>(a, stream);
+  if (a.res_bf16) return launch_norm_w<true, Res::kBf16>(a, stream);
+  return a.x_bf16 ? launch_norm_w<true, Res::kF32>(a, stream) : launch_norm_w<false, Res::kF32>(a, stream);
 }
 
 }  // namespace nvfp4
