@@ -50,9 +50,10 @@ def lib():
 
 
 # A decode call costs the host about as much as the GPU, so what every call
-# does is kept short: torch's own handle of the current stream, and checks by
-# attribute without helper objects.
+# does is kept short: torch's own calls for the current device and stream, and
+# checks by attribute without helper objects.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t):
@@ -66,17 +67,17 @@ def _code(table, dtype, what):
     return code
 
 
-def _stream(first, *others):
+def _stream(a, b=None, c=None, d=None, e=None, f=None):
     """The current stream of the current device, on which all the tensors have to be.
 
     (A stream that is being captured is refused by the library, before it
     launches anything.)"""
-    dev = first.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current GPU; got one on {first.device}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current GPU; got one on {t.device}")
+    dev = a.get_device()
+    if (dev < 0 or dev != _current_device() or (b is not None and b.get_device() != dev)
+            or (c is not None and c.get_device() != dev) or (d is not None and d.get_device() != dev)
+            or (e is not None and e.get_device() != dev) or (f is not None and f.get_device() != dev)):
+        where = ", ".join(str(t.device) for t in (a, b, c, d, e, f) if t is not None)
+        raise ValueError(f"tensors must be on the current GPU; got them on {where}")
     return _raw_stream(dev)
 
 
@@ -115,10 +116,9 @@ def _check_weight(codes, scales, zeros, group_size):
     want = (N, _groups(2 * half, group_size))
     if (codes.dtype != torch.uint8 or scales.dtype != torch.bfloat16 or scales.shape != want
             or (zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != want))):
-        raise ValueError(f"a packed weight is uint8 codes [N, K/2], bfloat16 scales [N, G] and uint8 zeros [N, G] or None, "
-                         f"G = {want[1]} for groups of {group_size}; got codes {codes.dtype} {tuple(codes.shape)}, scales "
-                         f"{scales.dtype} {tuple(scales.shape)}"
-                         + ("" if zeros is None else f", zeros {zeros.dtype} {tuple(zeros.shape)}"))
+        got = ", ".join(f"{t.dtype} {tuple(t.shape)}" for t in (codes, scales, zeros) if t is not None)
+        raise ValueError("a packed weight is uint8 codes [N, K/2], bfloat16 scales [N, G] and uint8 zeros [N, G] or "
+                         f"None, G = {want[1]} for groups of {group_size}; got {got}")
     if not (codes.is_contiguous() and scales.is_contiguous() and (zeros is None or zeros.is_contiguous())):
         raise ValueError("tensors must be contiguous")
     return N, 2 * half, want[1]
@@ -136,9 +136,9 @@ def quantize(w, group_size=128, symmetric=False, out=None):
     _contiguous(w)
     if out is None:
         stream = _stream(w)
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((N, G), dtype=torch.bfloat16, device=w.device)
-        zeros = None if symmetric else torch.empty((N, G), dtype=torch.uint8, device=w.device)
+        codes = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(N, G, dtype=torch.bfloat16, device=w.device)
+        zeros = None if symmetric else torch.empty(N, G, dtype=torch.uint8, device=w.device)
     else:
         codes, scales, zeros = out
         if (zeros is None) != bool(symmetric):
@@ -159,7 +159,7 @@ def dequant(codes, scales, zeros=None, group_size=128, out_dtype=torch.float32, 
     if out is None:
         dt = _code(_FLOATS, out_dtype, "output")
         stream = _stream(codes, scales, zeros)
-        out = torch.empty((N, K), dtype=out_dtype, device=codes.device)
+        out = torch.empty(N, K, dtype=out_dtype, device=codes.device)
     else:
         dt = _code(_FLOATS, out.dtype, "output")
         _given(out, (N, K), out.dtype)
@@ -184,7 +184,7 @@ def _product(x, codes, scales, zeros, group_size, out_dtype, out, x_scales=None)
     if out is None:
         dt = _code(_FLOATS, out_dtype, "output")
         stream = _stream(x, codes, scales, zeros, x_scales)
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = torch.empty(M, N, dtype=out_dtype, device=x.device)
     else:
         dt = _code(_FLOATS, out.dtype, "output")
         _given(out, (M, N), out.dtype)
@@ -212,8 +212,8 @@ def gemv_w4a8(x, x_scales, codes, scales, zeros=None, group_size=128, out_dtype=
     M, N, K, out, dt, stream = _product(x, codes, scales, zeros, group_size, out_dtype, out, x_scales)
     _done("int4_gemv_w4a8", lib().int4_gemv_w4a8(x.data_ptr(), xt, x_scales.data_ptr(),
                                                  0 if x_scales.shape[1] == 1 else group_size, codes.data_ptr(),
-                                                 scales.data_ptr(), _ptr(zeros), group_size, M, N, K, out.data_ptr(), dt,
-                                                 stream))
+                                                 scales.data_ptr(), _ptr(zeros), group_size, M, N, K,
+                                                 out.data_ptr(), dt, stream))
     return out
 
 
@@ -250,9 +250,9 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
             raise ValueError(f"weight must be a contiguous tensor of shape {(K,)}")
     if out is None:
         stream = _stream(x, weight, residual)
-        codes = torch.empty((M, K), dtype=out_dtype, device=x.device)
-        scales = torch.empty((M, G), dtype=torch.float32, device=x.device)
-        h = None if residual is None else torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        codes = torch.empty(M, K, dtype=out_dtype, device=x.device)
+        scales = torch.empty(M, G, dtype=torch.float32, device=x.device)
+        h = None if residual is None else torch.empty(M, K, dtype=residual.dtype, device=x.device)
     else:
         codes, scales, h = out
         if (h is None) != (residual is None):
@@ -263,6 +263,6 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
             _given(h, (M, K), residual.dtype, "out's sum")
         stream = _stream(x, weight, residual, codes, scales, h)
     _done("int4_rmsnorm_quant8",
-          lib().int4_rmsnorm_quant8(x.data_ptr(), xt, xs, _ptr(residual), rt, rs, _ptr(weight), wt, eps, M, K, group_size,
-                                    qt, codes.data_ptr(), scales.data_ptr(), _ptr(h), stream))
+          lib().int4_rmsnorm_quant8(x.data_ptr(), xt, xs, _ptr(residual), rt, rs, _ptr(weight), wt, eps, M, K,
+                                    group_size, qt, codes.data_ptr(), scales.data_ptr(), _ptr(h), stream))
     return codes, scales, h
