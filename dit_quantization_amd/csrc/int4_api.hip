@@ -18,7 +18,8 @@ using namespace nvfp4;
 // Rows of codes are addressed by 32-bit buffer offsets: 64 rows of 2^24
 // codes are 2^29 bytes, 16 rows of 2^24 bf16 activations as well.
 constexpr int64_t kMaxCols = (int64_t)1 << 24;
-constexpr int64_t kMaxN = (int64_t)1 << 30;
+// A launch counts its threads in 32 bits: 2^22 workgroups of 64 rows.
+constexpr int64_t kMaxN = (int64_t)1 << 28;
 constexpr int64_t kMaxNormCols = 65536;
 
 bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }

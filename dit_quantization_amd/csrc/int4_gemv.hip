@@ -5,8 +5,8 @@
 // turn 8 nibbles into 8 bytes, and such a byte is at once the INT8 value c
 // and the E4M3 value c / 512 (subnormals and the first binade are evenly
 // spaced).  INT8 activations meet them in integer products (exact inside a
-// group); for bf16 and E4M3 ones the FP8 converter makes exact bf16 pairs
-// c / 512, and the 512 goes into the scale.  The zero point is taken
+// group); for bf16 and E4M3 ones the FP8 converter, which multiplies by a
+// power of two on the way, makes exact bf16 pairs c.  The zero point is taken
 // off with the sum of x, which all rows of the weight share.
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
@@ -16,10 +16,6 @@ namespace nvfp4 {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPassSupers = 4;  // super-chunks of 128 codes a pass of the matrix kernel takes
-
-// What a product of bytes has to be multiplied by.
-template <Act A>
-constexpr float kUnit = A == Act::kI8 ? 1.0f : 512.0f;
 
 constexpr uint32_t kNibbles = 0x0F0F0F0Fu;
 
@@ -32,17 +28,23 @@ constexpr uint32_t kNibbles = 0x0F0F0F0Fu;
 template <Act A>
 struct Chunk {             // x of one chunk
   uint32_t x[A == Act::kI8 ? 8 : 16];
-  float sum;               // in units of the code products
+  float sum;
   float scale;
 };
 
 __device__ __forceinline__ float dot2_bf16(uint32_t a, uint32_t b, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
 }
+// Two E4M3 bytes (the low or the high half of w) as a bf16 pair, and two codes.
 __device__ __forceinline__ uint32_t pk_bf16_e4m3(uint32_t w, bool high) {
   return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true)
                                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
 }
+__device__ __forceinline__ uint32_t pk_bf16_code(uint32_t w, bool high) {
+  return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, true)
+                                           : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, false));
+}
+constexpr uint32_t kOnes = 0x3F803F80u;  // a bf16 pair
 
 template <Act A>
 __device__ __forceinline__ void load_chunk(Chunk<A>& c, __amdgpu_buffer_rsrc_t xbuf, int chunk, bool ok) {
@@ -67,13 +69,13 @@ __device__ __forceinline__ void load_chunk(Chunk<A>& c, __amdgpu_buffer_rsrc_t x
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       c.x[j] = A == Act::kBf16 ? raw[j] : pk_bf16_e4m3(raw[j / 2 % (BYTES / 4)], j & 1);
-      s = dot2_bf16(c.x[j], 0x3B003B00u, s);  // 2^-9 each
+      s = dot2_bf16(c.x[j], kOnes, s);
     }
     c.sum = s;
   }
 }
 
-// sum over a chunk of x (code - z), in kUnit
+// sum over a chunk of x (code - z)
 template <Act A>
 __device__ __forceinline__ float dot_chunk(const Chunk<A>& c, u32x4 w, float z) {
   if constexpr (A == Act::kI8) {
@@ -89,10 +91,10 @@ __device__ __forceinline__ float dot_chunk(const Chunk<A>& c, u32x4 w, float z) 
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const uint32_t lo = w[d] & kNibbles, hi = (w[d] >> 4) & kNibbles;
-      p[d & 1] = dot2_bf16(c.x[4 * d], pk_bf16_e4m3(lo, false), p[d & 1]);
-      p[d & 1] = dot2_bf16(c.x[4 * d + 1], pk_bf16_e4m3(lo, true), p[d & 1]);
-      p[d & 1] = dot2_bf16(c.x[4 * d + 2], pk_bf16_e4m3(hi, false), p[d & 1]);
-      p[d & 1] = dot2_bf16(c.x[4 * d + 3], pk_bf16_e4m3(hi, true), p[d & 1]);
+      p[d & 1] = dot2_bf16(c.x[4 * d], pk_bf16_code(lo, false), p[d & 1]);
+      p[d & 1] = dot2_bf16(c.x[4 * d + 1], pk_bf16_code(lo, true), p[d & 1]);
+      p[d & 1] = dot2_bf16(c.x[4 * d + 2], pk_bf16_code(hi, false), p[d & 1]);
+      p[d & 1] = dot2_bf16(c.x[4 * d + 3], pk_bf16_code(hi, true), p[d & 1]);
     }
     return __builtin_fmaf(-z, c.sum, p[0] + p[1]);
   }
@@ -171,7 +173,7 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 #pragma unroll
     for (int p = 1; p < S; ++p) sum += red[g * S + p][r];
     const int row = (blockIdx.x * GROUPS + g) * RW + r;
-    sum *= kUnit<A> * (A != Act::kBf16 && !x.grouped ? x.scales[0] : 1.0f);
+    if (A != Act::kBf16 && !x.grouped) sum *= x.scales[0];
     if (row < N) {
       if (bf16_out)
         reinterpret_cast<uint16_t*>(y)[row] = (uint16_t)f32_to_bf16_bits(sum);
@@ -219,12 +221,14 @@ struct Mfma {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0, 0,
                                                    0);
   }
-  static __device__ __forceinline__ X bytes(uint32_t a, uint32_t b) {
-    return X{pk_bf16_e4m3(a, false), pk_bf16_e4m3(a, true), pk_bf16_e4m3(b, false), pk_bf16_e4m3(b, true)};
+  static __device__ __forceinline__ X unpack(uint32_t w) {
+    const uint32_t lo = w & kNibbles, hi = (w >> 4) & kNibbles;
+    return X{pk_bf16_code(lo, false), pk_bf16_code(lo, true), pk_bf16_code(hi, false), pk_bf16_code(hi, true)};
   }
-  static __device__ __forceinline__ X unpack(uint32_t w) { return bytes(w & kNibbles, (w >> 4) & kNibbles); }
-  static __device__ __forceinline__ X of(u32x2 v) { return bytes(v.x, v.y); }
-  static __device__ __forceinline__ X ones() { return X{0x3B003B00u, 0x3B003B00u, 0x3B003B00u, 0x3B003B00u}; }
+  static __device__ __forceinline__ X of(u32x2 v) {  // 8 E4M3 activations
+    return X{pk_bf16_e4m3(v.x, false), pk_bf16_e4m3(v.x, true), pk_bf16_e4m3(v.y, false), pk_bf16_e4m3(v.y, true)};
+  }
+  static __device__ __forceinline__ X ones() { return X{kOnes, kOnes, kOnes, kOnes}; }
 };
 template <>
 struct Mfma<Act::kI8> {
@@ -555,7 +559,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
     for (int i = 0; i < 4; ++i) {
       const int m = 4 * (l >> 4) + i;
       if (m < M && n < N) {
-        const float v = sum[i] * (kUnit<A> * (A != Act::kBf16 && !x.grouped ? x.scales[m] : 1.0f));
+        const float v = A != Act::kBf16 && !GX ? sum[i] * x.scales[m] : sum[i];
         if (bf16_out)
           reinterpret_cast<uint16_t*>(y)[(int64_t)m * N + n] = (uint16_t)f32_to_bf16_bits(v);
         else

@@ -296,24 +296,39 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
 // 4096 x 4096, 256 x 2 25.4, 1024 x 1 28.1, 256 x 4 28.5; 2048 x 8192, 1024 x 1
 // 26.7, 256 x 4 30.5; 16384 x 1024, 64 x 2 25.4, 256 x 1 30.8.)
 template <bool XBF, Res RES, bool WBF>
-hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-  const int n8 = a.cols / 8;
-  const double ic = 1.0 / a.cols, it = a.e4m3 ? 1.0 / 448.0 : 1.0 / 127.0;
+hipError_t launch_norm(const NormArgs& all, hipStream_t stream) {
+  const int n8 = all.cols / 8, G = all.group ? (all.cols + all.group - 1) / all.group : 1;
+  const double ic = 1.0 / all.cols, it = all.e4m3 ? 1.0 / 448.0 : 1.0 / 127.0;
+  constexpr int HB = RES == Res::kNone ? 0 : RES == Res::kBf16 ? 2 : 4;  // bytes of a residual
+  // at most 2^20 workgroups a launch (a launch counts its threads in 32 bits)
+  const int64_t step = ((int64_t)1 << 20) * (n8 <= 16 ? 16 : n8 <= 128 ? 4 : 1);
+  for (int64_t r0 = 0; r0 < all.rows; r0 += step) {
+    NormArgs a = all;
+    a.rows = all.rows - r0 < step ? all.rows - r0 : step;
+    a.x = reinterpret_cast<const char*>(all.x) + r0 * all.x_stride * (XBF ? 2 : 4);
+    if (RES != Res::kNone) {
+      a.residual = reinterpret_cast<const char*>(all.residual) + r0 * all.res_stride * HB;
+      a.residual_out = reinterpret_cast<char*>(all.residual_out) + r0 * all.cols * HB;
+    }
+    a.codes = reinterpret_cast<char*>(all.codes) + r0 * all.cols;
+    a.scales = all.scales + r0 * G;
 #define NORM_CASE(T, V)                                                                                  \
   hipLaunchKernelGGL((rmsnorm_quant_kernel<T, V, XBF, RES, WBF>),                                        \
                      dim3((unsigned)((a.rows + (T < 256 ? 256 / T : 1) - 1) / (T < 256 ? 256 / T : 1))), \
                      dim3(T < 256 ? 256 : T), 0, stream, a, ic, it)
-  if (n8 <= 16) NORM_CASE(16, 1);
-  else if (n8 <= 64) NORM_CASE(64, 1);
-  else if (n8 <= 128) NORM_CASE(64, 2);
-  else if (n8 <= 256) NORM_CASE(256, 1);
-  else if (n8 <= 512) NORM_CASE(256, 2);
-  else if (n8 <= 1024) NORM_CASE(1024, 1);
-  else if (n8 <= 2048) NORM_CASE(1024, 2);
-  else if (n8 <= 4096) NORM_CASE(1024, 4);
-  else NORM_CASE(1024, 8);
+    if (n8 <= 16) NORM_CASE(16, 1);
+    else if (n8 <= 64) NORM_CASE(64, 1);
+    else if (n8 <= 128) NORM_CASE(64, 2);
+    else if (n8 <= 256) NORM_CASE(256, 1);
+    else if (n8 <= 512) NORM_CASE(256, 2);
+    else if (n8 <= 1024) NORM_CASE(1024, 1);
+    else if (n8 <= 2048) NORM_CASE(1024, 2);
+    else if (n8 <= 4096) NORM_CASE(1024, 4);
+    else NORM_CASE(1024, 8);
 #undef NORM_CASE
-  return hipGetLastError();
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool XBF, Res RES>

@@ -81,7 +81,7 @@ int int4_dequant(const uint8_t* codes, const void* scales, const uint8_t* zeros,
  *   x [M, K] bf16, 16-byte aligned; codes [N, K/2], 16-byte aligned; scales
  *   [N, G], 2-byte aligned; zeros [N, G] or NULL; y [M, N] of y_dtype
  *   (NVFP4_BF16 or NVFP4_F32), 4-byte aligned
- *   0 <= M <= 16; K % 32 == 0, 0 < K <= 2^24; N <= 2^30, otherwise
+ *   0 <= M <= 16; K % 32 == 0, 0 < K <= 2^24; N <= 2^28, otherwise
  *   NVFP4_ERR_UNSUPPORTED (K % 16 != 0: NVFP4_ERR_SHAPE).  fp32 accumulation
  *   in a fixed order (results are reproducible), RNE bf16 output.
  */

@@ -154,6 +154,24 @@ def check_product(kind, M, N, K, group, symmetric, grouped, dtype, seed):
     return y
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M", [1, 4])
+def test_products_of_small_values(kind, M):
+    """Values and scales near the lower end of fp32's normal range lose nothing:
+    powers of two times a call's inputs give the same result times them."""
+    hw, w = packed_weight(48, 640, 64, False, 31)
+    args, _ = activations(kind, M, 640, 64, False, 32)
+    y = call(kind, args, w, 64, FL)
+    tiny = 2.0 ** -96
+    if kind == "bf16":
+        small = call(kind, (args[0] * tiny,), w, 64, FL)
+    else:
+        small = call(kind, (args[0], args[1] * tiny), w, 64, FL)
+    assert torch.equal(small, y * tiny)
+    small = call(kind, args, (w[0], w[1] * tiny, w[2]), 64, FL)
+    assert torch.equal(small, y * tiny)
+
+
 # M, N, K: one row and one block; rows that end inside a group; odd N; each
 # count of rows; lengths that no power of two divides; every kernel's range
 SHAPES = [(1, 1, 32), (1, 7, 96), (1, 64, 256), (1, 129, 4128), (1, 65, 14336), (1, 5, 33824), (2, 33, 160), (3, 16, 32),
@@ -345,7 +363,43 @@ def test_norm_strides_in_place_and_guards():
         int4.rmsnorm_quant8(torch.zeros((1, 16), dtype=BF, device=DEV).expand(4, 16))
 
 
+def test_norm_of_more_rows_than_one_launch_takes():
+    """2^24 + 5 rows of 16 columns: the rows of either launch as if alone."""
+    rows = (1 << 24) + 5
+    print(f"[case] norm {rows}x16", flush=True)
+    x = torch.randn((rows, 16), device=DEV, dtype=BF, generator=torch.Generator(DEV).manual_seed(1))
+    r, wt = x.flip(0).contiguous(), torch.linspace(0.5, 1.5, 16, device=DEV)
+    whole = int4.rmsnorm_quant8(x, wt, residual=r)
+    for part in (slice(0, 1000), slice((1 << 24) - 500, rows)):
+        alone = int4.rmsnorm_quant8(x[part], wt, residual=r[part])
+        assert all(torch.equal(a[part], b) for a, b in zip(whole, alone))
+
+
 # ---- together, and as a caller may use them
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 elements, and codes of more than 2^31 bytes:
+    the last rows as if alone."""
+    rows, cols = (1 << 19) + 3, 8192 + 32
+    print(f"[case] {rows}x{cols}", flush=True)
+    x = torch.randn((rows, cols), device=DEV, dtype=BF, generator=torch.Generator(DEV).manual_seed(2))
+    last = slice(rows - 70, rows)
+    w = int4.quantize(x, 128)
+    part = int4.quantize(x[last], 128)
+    assert all(torch.equal(a[last], b) for a, b in zip(w, part))
+    assert torch.equal(int4.dequant(*w, out_dtype=BF)[last], int4.dequant(*part, out_dtype=BF))
+    q, s, _ = int4.rmsnorm_quant8(x, group_size=128)
+    q1, s1, _ = int4.rmsnorm_quant8(x[last], group_size=128)
+    assert torch.equal(q[last], q1) and torch.equal(s[last], s1)
+    del x
+    for M in (1, 3):
+        v = q[:M].contiguous(), s[:M].contiguous()
+        y, y1 = int4.gemv_w4a8(*v, *w, out_dtype=FL), int4.gemv_w4a8(*v, *part, out_dtype=FL)
+        # other shapes of the call may add in another order
+        a = torch.from_numpy(ref.product(q[:M].cpu().numpy() * ref.per_element(f32(s[:M]), cols, 128),
+                                         ref.unpack(part[0].cpu().numpy()), f32(part[1]), part[2].cpu().numpy(), 128)[1])
+        assert np.all(np.abs(f32(y[:, last]) - f32(y1)) <= 2 * ref.product_bound(a.numpy(), cols))
 
 def test_decode_mlp():
     """Norm, gate and up products on its codes, activation, down product in 16

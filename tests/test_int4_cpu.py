@@ -71,7 +71,7 @@ def test_gemv_validation():
         assert f(dt=int4.I8) == nv.ERR_DTYPE
         assert f(M=-1) == f(N=-1) == f(K=40) == f(K=-32) == nv.ERR_SHAPE
         assert f(M=17) == f(K=48) == f(K=0) == f(group=48) == f(K=(1 << 24) + 32) == nv.ERR_UNSUPPORTED
-        assert f(N=(1 << 30) + 1) == nv.ERR_UNSUPPORTED
+        assert f(N=(1 << 28) + 1) == nv.ERR_UNSUPPORTED
         assert f(x=A + 8) == f(codes=A + 4) == f(scales=A + 1) == f(y=A + 2) == nv.ERR_ALIGN
         assert f(x=None, codes=None, scales=None, zeros=None, y=None, M=0) == nv.OK
         assert f(x=None, codes=None, scales=None, zeros=None, y=None, N=0) == nv.OK
