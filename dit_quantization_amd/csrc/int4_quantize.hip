@@ -1,36 +1,39 @@
 // Group-scaled 4-bit integer weights (format: include/int4.h): the quantizer
-// and its inverse.  Both stream: a lane holds 8 consecutive elements (one
-// dword of codes) and a group of 32, 64 or 128 is 4, 8 or 16 neighbouring
-// lanes, so its range is a few lane exchanges.  A wave takes runs of 64
-// vectors of one row; where rows end on a group (the usual case) the whole
-// tensor is one such row.
+// and its inverse.  Both stream, bound by memory.  In the quantizer a lane holds
+// a vector of 8 consecutive elements (one dword of codes) and a group of 32,
+// 64 or 128 is 4, 8 or 16 neighbouring lanes, so its range is a few lane
+// exchanges.  A wave takes runs of 64 vectors of one row; where rows end on a
+// group (the usual case) the whole tensor is one such row.
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
 #include "lanes.hpp"
 
 namespace nvfp4 {
 
-// Runs of 64 vectors that a wave keeps in flight.  (us, 14336 x 4096: fp32
-// quantize 50.1, 50.2, 51.2 with 1, 2, 4; bf16 38.5, 32.6, 31.8; dequant to
-// bf16 39.9, 33.9, 32.7; to fp32, whose stores are twice as wide, 57.9, 57.2,
-// 76.2.  1024 x 4096 bf16 quantize 4.7, 4.4, 5.1.)
-constexpr int kQuantizeRuns = 2, kDequantRunsBf16 = 4, kDequantRunsF32 = 2;
+// Runs of 64 vectors that a wave keeps in flight, and whether inputs are read
+// non-temporally, from a sweep over both (us, weights read again after 3 others
+// / after 14):
+//   quantize 14336 x 4096 fp32: 1 run 47.1 / 47.1; 2 runs 48.5 / 48.6; 1 run
+//   non-temporal 49.9 / 51.3.  bf16: 2 runs non-temporal 32.6 / 33.3, 1 run 38;
+//   1024 x 4096 bf16: 2 runs non-temporal 4.3, temporal 4.8, 4 runs 5.2.
+//   dequant 14336 x 4096 to bf16: 4 runs 23.2 / 32.3, 2 runs 22.9 / 33.4; 4 runs
+//   non-temporal 32.8 / 32.7; to fp32: 2 runs 37.0 / 54.8, 4 runs 39.3 / 55.4.
+constexpr int kQuantizeRunsF32 = 1, kQuantizeRunsBf16 = 2, kDequantRunsF32 = 2, kDequantRunsBf16 = 4;
 
 // The rows a launch sees: the tensor's own, or one of all its elements.
 struct RowView {
-  int64_t rows, n8, padded8;  // vectors of a row, and that rounded up to whole groups
-  int64_t runs;               // runs of 64 vectors of a row
-  int64_t units;              // as many runs of a row as a wave keeps in flight, each
+  int64_t rows, nv, padded;  // vectors of a row, and that rounded up to whole groups
+  int64_t units;             // as many runs of a row as a wave keeps in flight, each
 };
 
-static RowView row_view(int64_t rows, int64_t cols, int group, int runs) {
+// per: elements of a vector
+static RowView row_view(int64_t rows, int64_t cols, int group, int per, int runs) {
   RowView v;
   const bool flat = cols % group == 0;
   v.rows = flat ? 1 : rows;
-  v.n8 = (flat ? rows * cols : cols) / 8;
-  v.padded8 = (v.n8 + group / 8 - 1) / (group / 8) * (group / 8);
-  v.runs = (v.padded8 + 63) / 64;
-  v.units = (v.runs + runs - 1) / runs;
+  v.nv = (flat ? rows * cols : cols) / per;
+  v.padded = (v.nv + group / per - 1) / (group / per) * (group / per);
+  v.units = ((v.padded + 63) / 64 + runs - 1) / runs;
   return v;
 }
 
@@ -39,8 +42,12 @@ struct Raw {
   u32x4 a[BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const void* x, int64_t vec) {
     const u32x4* p = reinterpret_cast<const u32x4*>(x) + (BF16 ? vec : 2 * vec);
-    a[0] = __builtin_nontemporal_load(p);
-    if (!BF16) a[BF16 ? 0 : 1] = __builtin_nontemporal_load(p + 1);
+    if (BF16) {
+      a[0] = __builtin_nontemporal_load(p);
+    } else {
+      a[0] = p[0];
+      a[BF16 ? 0 : 1] = p[1];
+    }
   }
   __device__ __forceinline__ void zero() {
     a[0] = u32x4{0, 0, 0, 0};
@@ -88,7 +95,7 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
     Raw<BF16> raw[RUNS];
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-      if (v0 + 64 * k < rv.n8) raw[k].load(x, row * rv.n8 + v0 + 64 * k);
+      if (v0 + 64 * k < rv.nv) raw[k].load(x, row * rv.nv + v0 + 64 * k);
       else raw[k].zero();
     }
 #pragma unroll
@@ -143,8 +150,8 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
         const float c1 = __builtin_amdgcn_fmed3f(t[4 + b] + z, 0.0f, 15.0f);
         word |= (uint32_t)__builtin_fmaf(c1, 16.0f, c0) << (8 * b);
       }
-      if (v < rv.n8) {
-        reinterpret_cast<uint32_t*>(codes)[row * rv.n8 + v] = word;
+      if (v < rv.nv) {
+        reinterpret_cast<uint32_t*>(codes)[row * rv.nv + v] = word;
         if ((lane & (L - 1)) == 0) {
           const int64_t slot = row * G + v / L;
           scales[slot] = (uint16_t)sb;
@@ -155,11 +162,14 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
   }
 }
 
+// A lane makes 16 bytes: 8 bf16 values of a dword of codes, or the 4 fp32
+// values of its low or its high nibbles (then two lanes read one dword).
 template <bool BF16, int RUNS>
 __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __restrict__ codes,
                                                            const uint16_t* __restrict__ scales,
                                                            const uint8_t* __restrict__ zeros, RowView rv, int L,
                                                            int64_t G, void* __restrict__ out) {
+  constexpr int HALVES = BF16 ? 1 : 2;
   const int lane = threadIdx.x & 63;
   const int64_t n_units = rv.rows * rv.units;
   for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
@@ -169,9 +179,9 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
     uint32_t w[RUNS], sb[RUNS], z[RUNS];
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
-      const int64_t v = min(v0 + 64 * k, rv.n8 - 1);
+      const int64_t v = min(v0 + 64 * k, rv.nv - 1);
       const int64_t slot = row * G + v / L;
-      w[k] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(codes) + row * rv.n8 + v);
+      w[k] = reinterpret_cast<const uint32_t*>(codes)[(row * rv.nv + v) / HALVES];
       sb[k] = scales[slot];
       z[k] = zeros ? zeros[slot] : 8u;
     }
@@ -179,21 +189,17 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
     for (int k = 0; k < RUNS; ++k) {
       const int64_t v = v0 + 64 * k;
       const float s = bf16_bits_to_f32(sb[k]), zf = (float)z[k];
-      const uint32_t lo = w[k] & 0x0F0F0F0Fu, hi = (w[k] >> 4) & 0x0F0F0F0Fu;
-      float f[8];
+      const uint32_t half[2] = {(BF16 || (lane & 1) == 0 ? w[k] : w[k] >> 4) & 0x0F0F0F0Fu, (w[k] >> 4) & 0x0F0F0F0Fu};
+      float f[8 / HALVES];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = s * ((float)(((j < 4 ? lo : hi) >> (8 * (j & 3))) & 0xFFu) - zf);
-      if (v >= rv.n8) continue;
-      if (BF16) {
-        u32x4 o;
+      for (int j = 0; j < 8 / HALVES; ++j) f[j] = s * ((float)((half[j / 4] >> (8 * (j & 3))) & 0xFFu) - zf);
+      if (v >= rv.nv) continue;
+      u32x4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = f32_to_bf16_bits(f[2 * j]) | (f32_to_bf16_bits(f[2 * j + 1]) << 16);
-        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(out) + row * rv.n8 + v);
-      } else {
-        f32x4* o = reinterpret_cast<f32x4*>(out) + 2 * (row * rv.n8 + v);
-        __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, o);
-        __builtin_nontemporal_store(f32x4{f[4], f[5], f[6], f[7]}, o + 1);
-      }
+      for (int j = 0; j < 4; ++j)
+        o[j] = BF16 ? f32_to_bf16_bits(f[BF16 ? 2 * j : 0]) | (f32_to_bf16_bits(f[BF16 ? 2 * j + 1 : 0]) << 16)
+                    : __float_as_uint(f[j]);
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(out) + row * rv.nv + v);
     }
   }
 }
@@ -205,24 +211,25 @@ static dim3 stream_grid(const RowView& v) {
 
 hipError_t launch_int4_quantize(const void* x, bool bf16, int64_t rows, int64_t cols, int group, uint8_t* codes,
                                 uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const RowView v = row_view(rows, cols, group, kQuantizeRuns);
+  const RowView v = row_view(rows, cols, group, 8, bf16 ? kQuantizeRunsBf16 : kQuantizeRunsF32);
   const int64_t G = (cols + group - 1) / group;
 #define INT4_QUANTIZE(B, R)                                                                                        \
   hipLaunchKernelGGL((int4_quantize_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, x, v, group / 8, G, codes, \
                      scales, zeros)
-  if (bf16) INT4_QUANTIZE(true, kQuantizeRuns);
-  else INT4_QUANTIZE(false, kQuantizeRuns);
+  if (bf16) INT4_QUANTIZE(true, kQuantizeRunsBf16);
+  else INT4_QUANTIZE(false, kQuantizeRunsF32);
 #undef INT4_QUANTIZE
   return hipGetLastError();
 }
 
 hipError_t launch_int4_dequant(const Int4Weight& w, int64_t rows, int64_t cols, void* out, bool bf16_out,
                                hipStream_t stream) {
-  const RowView v = row_view(rows, cols, w.group, bf16_out ? kDequantRunsBf16 : kDequantRunsF32);
+  const RowView v = bf16_out ? row_view(rows, cols, w.group, 8, kDequantRunsBf16)
+                             : row_view(rows, cols, w.group, 4, kDequantRunsF32);
   const int64_t G = (cols + w.group - 1) / w.group;
 #define INT4_DEQUANT(B, R)                                                                                             \
   hipLaunchKernelGGL((int4_dequant_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, w.codes, w.scales, w.zeros, v, \
-                     w.group / 8, G, out)
+                     w.group / (B ? 8 : 4), G, out)
   if (bf16_out) INT4_DEQUANT(true, kDequantRunsBf16);
   else INT4_DEQUANT(false, kDequantRunsF32);
 #undef INT4_DEQUANT
