@@ -101,14 +101,14 @@ int int4_gemv_w4a8(const void* x, int x_dtype, const float* x_scales, int x_grou
 int int4_rmsnorm_quant8(const void* x, int x_dtype, int64_t x_stride, const void* residual, int res_dtype,
                         int64_t res_stride, const void* weight, int w_dtype, double eps, int64_t rows, int64_t cols,
                         int group, int q_dtype, void* codes, float* scales, void* residual_out, void* stream) {
-  const bool empty = rows == 0 || cols == 0;
+  const bool empty = rows == 0;
   if (!empty && (!x || !codes || !scales || (residual && !residual_out))) return NVFP4_ERR_NULL;
   if (x_dtype != NVFP4_F32 && x_dtype != NVFP4_BF16) return NVFP4_ERR_DTYPE;
   if (residual && res_dtype != x_dtype && res_dtype != NVFP4_F32) return NVFP4_ERR_DTYPE;
   if (weight && w_dtype != NVFP4_F32 && w_dtype != NVFP4_BF16) return NVFP4_ERR_DTYPE;
   if (q_dtype != INT4_I8 && q_dtype != INT4_E4M3) return NVFP4_ERR_DTYPE;
   if (!(eps >= 0.0) || std::isinf(eps)) return NVFP4_ERR_FLAGS;
-  if (rows < 0 || cols < 0 || cols % 16 != 0) return NVFP4_ERR_SHAPE;
+  if (rows < 0 || cols <= 0 || cols % 16 != 0) return NVFP4_ERR_SHAPE;
   if (x_stride < cols || !mul_ok(rows, x_stride)) return NVFP4_ERR_SHAPE;
   if (residual && (res_stride < cols || !mul_ok(rows, res_stride))) return NVFP4_ERR_SHAPE;
   if (cols > kMaxNormCols || (group != 0 && !group_ok(group))) return NVFP4_ERR_UNSUPPORTED;

@@ -305,7 +305,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   // 9.8 us instead of 9.2).
   __shared__ u32x4 lds_c0[NW][256], lds_c1[NW][256], lds_c2[NW][256], lds_c3[NW][256];
   __shared__ u32x4 lds_x[NW][256];
-  __shared__ uint32_t lds_s[NW][T == 1 ? 28 * NG : 1];
+  __shared__ __align__(16) uint32_t lds_s[NW][T == 1 ? 28 * NG : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const auto tile = [&](int t) {  // t is a constant once the loops are unrolled
     return t == 0 ? lds_c0[wave] : t == 1 ? lds_c1[wave] : t == 2 ? lds_c2[wave] : lds_c3[wave];

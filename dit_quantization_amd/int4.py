@@ -217,10 +217,12 @@ def gemv_w4a8(x, x_scales, codes, scales, zeros=None, group_size=128, out_dtype=
     return out
 
 
-def _row_stride(t, what):
-    if t.stride(1) != 1 and t.shape[1] > 1:
+def _row_stride(t, cols, what):
+    if t.is_contiguous():
+        return cols
+    if t.stride(1) != 1 and cols > 1:
         raise ValueError(f"{what}'s rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return t.stride(0) if t.shape[0] > 1 else cols
 
 
 def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dtype=torch.int8, out=None):
@@ -234,16 +236,18 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
     16-byte units (slices of wider tensors).
     out: the three tensors to write instead; the third may be the residual or
     x itself where type and layout agree (the sum in place)."""
-    M, K = _matrix(x, "x")
-    xt, qt = _code(_FLOATS, x.dtype, "x"), _code(_BYTES, out_dtype if out is None else out[0].dtype, "output")
+    M, K = shape = _matrix(x, "x")
+    xdt = x.dtype
+    xt, qt = _code(_FLOATS, xdt, "x"), _code(_BYTES, out_dtype if out is None else out[0].dtype, "output")
     if not 0 <= eps < math.inf:
         raise ValueError(f"eps={eps}: expected a finite value >= 0")
     G = _groups(K, group_size) if group_size else 1
-    xs, rt, rs, wt = _row_stride(x, "x"), F32, 0, F32
+    xs, rt, rs, wt = _row_stride(x, K, "x"), F32, 0, F32
     if residual is not None:
-        if residual.shape != x.shape or (residual.dtype != x.dtype and residual.dtype != torch.float32):
+        rdt = residual.dtype
+        if residual.shape != shape or (rdt != xdt and rdt != torch.float32):
             raise ValueError(f"residual must have x's shape {(M, K)} and its type or float32")
-        rt, rs = _FLOATS[residual.dtype], _row_stride(residual, "residual")
+        rt, rs = _FLOATS[rdt], _row_stride(residual, K, "residual")
     if weight is not None:
         wt = _code(_FLOATS, weight.dtype, "weight")
         if weight.shape != (K,) or not weight.is_contiguous():
@@ -252,7 +256,7 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
         stream = _stream(x, weight, residual)
         codes = torch.empty(M, K, dtype=out_dtype, device=x.device)
         scales = torch.empty(M, G, dtype=torch.float32, device=x.device)
-        h = None if residual is None else torch.empty(M, K, dtype=residual.dtype, device=x.device)
+        h = None if residual is None else torch.empty(M, K, dtype=rdt, device=x.device)
     else:
         codes, scales, h = out
         if (h is None) != (residual is None):

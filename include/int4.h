@@ -121,7 +121,7 @@ int int4_gemv_w4a8(const void* x, int x_dtype, const float* x_scales, int x_grou
  *   codes    [rows, cols] contiguous; scales fp32 [rows, 1 or ceil(cols/group)]
  *   residual_out [rows, cols] contiguous of res_dtype: h; it may be the
  *            residual or x itself (in place) where type and strides agree
- *   cols % 16 == 0 and strides >= cols (NVFP4_ERR_SHAPE otherwise), cols <=
+ *   cols % 16 == 0, cols > 0 and strides >= cols (else NVFP4_ERR_SHAPE), cols <=
  *   65536 (NVFP4_ERR_UNSUPPORTED), eps finite and >= 0 (NVFP4_ERR_FLAGS);
  *   pointers and rows 16-byte aligned (codes 8, scales 4).
  */

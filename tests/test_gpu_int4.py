@@ -14,6 +14,7 @@ from tests import int4_reference as ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+BF, FL = torch.bfloat16, torch.float32
 HALF_BF16 = 2.0 ** -8                    # half a step, relative
 
 
@@ -176,7 +177,8 @@ def test_products_of_small_values(kind, M):
 # count of rows; lengths that no power of two divides; every kernel's range
 SHAPES = [(1, 1, 32), (1, 7, 96), (1, 64, 256), (1, 129, 4128), (1, 65, 14336), (1, 5, 33824), (2, 33, 160), (3, 16, 32),
           (4, 100, 1024), (5, 17, 544), (7, 8193, 128), (8, 31, 4096), (11, 40, 14336), (16, 1, 64), (16, 200, 2080),
-          (16, 8200, 256), (1, 9000, 128), (13, 1025, 992)]
+          (16, 8200, 256), (1, 9000, 128), (13, 1025, 992), (3, 5000, 192), (16, 4112, 1056), (6, 8190, 512),
+          (1, 3000, 8224), (1, 4099, 160), (2, 48, 8704)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -248,6 +250,21 @@ def test_products_write_only_their_outputs_and_repeat():
                 assert torch.equal(buf[64:64 + M * N].view(M, N), f(*args, *w, group_size=64, out_dtype=dt))
 
 
+@pytest.mark.parametrize("M,N", [(1, 40), (1, 4200), (4, 40), (9, 4200), (16, 8300)])
+def test_products_with_scales_anywhere(M, N):
+    """Scales and zero points at any address their types allow give the same."""
+    for kind in ("bf16", "int8"):
+        _, (c, s, z) = packed_weight(N, 1024, 128, False, 41)
+        args, _ = activations(kind, M, 1024, 128, True, 42)
+        y = call(kind, args, (c, s, z), 128, FL)
+        s2, z2 = torch.empty(s.numel() + 9, dtype=BF, device=DEV), torch.empty(z.numel() + 9, dtype=torch.uint8, device=DEV)
+        for i in (1, 2, 3):
+            a, b = s2[i:i + s.numel()].view_as(s), z2[i:i + z.numel()].view_as(z)
+            a.copy_(s)
+            b.copy_(z)
+            assert torch.equal(call(kind, args, (c, a, b), 128, FL), y)
+
+
 def test_rows_do_not_depend_on_each_other():
     """A row of zeros and a loud row beside others leave them as they are."""
     _, w = packed_weight(70, 512, 128, False, 9)
@@ -288,9 +305,6 @@ def check_norm(x, r, wt, eps, group, dtype, out=None):
 
 
 COLS = [16, 48, 64, 128, 144, 272, 1040, 2048, 2064, 4096, 8208, 14336, 16400, 65536]
-BF, FL = torch.bfloat16, torch.float32
-
-
 @pytest.mark.parametrize("dtype", [torch.int8, torch.float8_e4m3fn], ids=["int8", "e4m3"])
 @pytest.mark.parametrize("cols", COLS)
 def test_norm(cols, dtype):

@@ -98,7 +98,7 @@ def test_rmsnorm_validation():
     assert call(x=A + 8) == call(r=A + 8) == call(h=A + 8) == call(w=A + 8) == call(q=A + 4) == nv.ERR_ALIGN
     assert call(s=A + 2) == call(xs=68) == call(rs=68) == nv.ERR_ALIGN    # rows of 136 bytes
     assert call(rows=0, x=None, r=None, w=None, q=None, s=None, h=None) == nv.OK
-    assert call(cols=0, xs=0, rs=0) == nv.OK
+    assert call(cols=0, xs=0, rs=0) == nv.ERR_SHAPE                       # a norm of nothing
 
 
 def _weight(N=8, K=64, G=2):
