@@ -186,15 +186,13 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // ---- several rows: 16 x 16 x 32 matrix instructions.
 // A workgroup of NW waves owns 16 T weight rows; its waves split K into runs
 // of super-chunks of 128 codes, 4 to a pass.  The codes of a pass reach LDS by
-// DMA, every instruction reading 4 rows x 256 contiguous bytes, and lane
-// (n, g) (n = lane % 16, g = lane / 16) reads back the 32 codes of one chunk
-// of row n from a row-swizzled slot.  A matrix instruction adds up over the
-// lane groups g, and which 8 of the 128 codes each group feeds it is free as
-// long as x agrees and all 32 belong to one scale group: 8 each for bf16 and
-// groups of 32 (instruction j takes chunk j), 16 each for two instructions of
-// 8-bit activations (j / 2 takes half a super-chunk).  The dwords of the codes
-// trade places between lane groups accordingly (v_permlane16_swap and
-// v_permlane32_swap, one or two steps of a 4 x 4 transpose).
+// DMA, every instruction reading 4 rows x 256 contiguous bytes, the 16-byte
+// chunks of a row swizzled so that no read back has bank conflicts.  A matrix
+// instruction adds up over the lane groups g (lane = 16 g + n, n a row of the
+// weight), and which 8 of the 128 codes each group feeds it is free as long as
+// x agrees and all 32 belong to one scale group: a dword each of one chunk for
+// bf16 and for groups of 32, and for 8-bit activations two dwords each of half
+// a super-chunk for two instructions, so that 16 bytes of x serve both.
 //
 // Reading x costs as much as reading the codes: every workgroup reads all of
 // it, from L2, and a load instruction takes the same 16 cycles of the address
@@ -241,29 +239,6 @@ struct Mfma<Act::kI8> {
   static __device__ __forceinline__ X of(u32x2 v) { return v; }
   static __device__ __forceinline__ X ones() { return X{0x01010101u, 0x01010101u}; }
 };
-
-// Bits of a code's place: lane group g = (g1, g0), dword d = (d1, d0) of its
-// chunk.  In pairs: lane group g reads chunk (g0, g1), and trading g0 with d1
-// leaves instruction j = (j1, j0) with dword 2 g + j0 of half super-chunk j1.
-// One by one: lane group g reads chunk g, and trading both bits leaves
-// instruction j with dword g of chunk j.
-template <bool PAIRS>
-__device__ __forceinline__ int chunk_of(int g) { return PAIRS ? 2 * (g & 1) + (g >> 1) : g; }
-
-template <bool PAIRS>
-__device__ __forceinline__ u32x4 regroup(u32x4 d) {
-  if constexpr (PAIRS) {
-    const auto a = __builtin_amdgcn_permlane16_swap(d[0], d[2], false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(d[1], d[3], false, false);
-    return u32x4{a[0], b[0], a[1], b[1]};
-  } else {
-    const auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
-    const auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    return u32x4{e[0], e[1], f[0], f[1]};
-  }
-}
 
 // LDS written by other lanes of the wave is read after this (a wave's LDS
 // operations complete in order: only the compiler has to keep it).
@@ -467,6 +442,30 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
     }
   };
 
+  // The dwords of codes this lane feeds to the four matrix instructions of
+  // super-chunk u: instruction j takes dword g of chunk j, or, in pairs, dword
+  // 2 (g & 1) + j % 2 of chunk 2 (j / 2) + g / 2.
+  // (Byte 256 n + 16 (chunk ^ n) + 4 dword of the tile: u and j are constants,
+  // so an address is one exclusive or; made anew for every pass, since kept
+  // they would cost 16 registers.)
+  int code_at = PAIRS ? 256 * nl + 16 * (nl ^ (g >> 1)) + 8 * (g & 1) : 272 * nl + 4 * g;
+  const auto codes_of = [&](int t, int u) {
+    const char* const codes = reinterpret_cast<const char*>(tile(t));
+    u32x4 d;
+#pragma unroll
+    for (int j = 0; j < 4; j += PAIRS ? 2 : 1) {
+      const char* const at = codes + (code_at ^ (64 * u + 16 * j));
+      if constexpr (PAIRS) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(at);
+        d[j] = v.x;
+        d[j + 1] = v.y;
+      } else {
+        d[j] = *reinterpret_cast<const uint32_t*>(at);
+      }
+    }
+    return d;
+  };
+
   // Scales, zero points and grouped scales of x to LDS.
   const auto spread_scales = [&](const P& p) {
     wave_fence();
@@ -486,8 +485,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   };
 
   // Products of super-chunk u of tile t.
-  const auto multiply = [&](int t, int u, u32x4 codes, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
-    const u32x4 d = regroup<PAIRS>(codes);
+  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int at = u * PER + q;
@@ -518,7 +516,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
         spread(p, v, xa, xs);
 #pragma unroll
         for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u)
-          multiply(0, u, tile(0)[16 * nl + ((4 * u + chunk_of<PAIRS>(g)) ^ nl)], xa, xs);
+          multiply(0, u, codes_of(0, u), xa, xs);
       }
     } else {
       // tile by tile, in the order of the DMA, so that a tile's products
@@ -531,7 +529,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
         __builtin_amdgcn_sched_barrier(0);
         u32x4 cw[SW];
 #pragma unroll
-        for (int u = 0; u < SW; ++u) cw[u] = tile(t)[16 * nl + ((4 * u + chunk_of<PAIRS>(g)) ^ nl)];
+        for (int u = 0; u < SW; ++u) cw[u] = codes_of(t, u);
 #pragma unroll
         for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa, xs);
       }
@@ -539,6 +537,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   };
 
   for (int s0 = sbeg; s0 < send; s0 += SW) {  // wave-uniform
+    asm volatile("" : "+v"(code_at));
     P p;
     load(p, s0);
     compute(p);

@@ -241,6 +241,7 @@ def rmsnorm_quant8(x, weight=None, residual=None, eps=1e-6, group_size=0, out_dt
     xt, qt = _code(_FLOATS, xdt, "x"), _code(_BYTES, out_dtype if out is None else out[0].dtype, "output")
     if not 0 <= eps < math.inf:
         raise ValueError(f"eps={eps}: expected a finite value >= 0")
+    group_size = group_size or 0
     G = _groups(K, group_size) if group_size else 1
     xs, rt, rs, wt = _row_stride(x, K, "x"), F32, 0, F32
     if residual is not None:
