@@ -24,7 +24,9 @@ constexpr uint32_t kNibbles = 0x0F0F0F0Fu;
 // each.  Lane l of a wave has the 16-byte chunks (32 codes, inside one group)
 // l, l + 64, ... of its K part, so one load instruction reads 1 KB of a row,
 // and keeps the x of its chunks and their sums in registers for all its rows.
-// Loads past the K part, or of rows past N, return zeros.
+// Loads past the K part, or of rows past N, return zeros.  Bound by latency at
+// the sizes that come here: 1024 x 4096, INT8, 3.3 us (2.2 MB), where an empty
+// kernel takes 2.5.
 template <Act A>
 struct Chunk {             // x of one chunk
   uint32_t x[A == Act::kI8 ? 8 : 16];
@@ -190,9 +192,9 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // chunks of a row swizzled so that no read back has bank conflicts.  A matrix
 // instruction adds up over the lane groups g (lane = 16 g + n, n a row of the
 // weight), and which 8 of the 128 codes each group feeds it is free as long as
-// x agrees and all 32 belong to one scale group: a dword each of one chunk for
-// bf16 and for groups of 32, and for 8-bit activations two dwords each of half
-// a super-chunk for two instructions, so that 16 bytes of x serve both.
+// x agrees and all 32 belong to one scale group: two dwords each of half a
+// super-chunk for two instructions (one 8-byte read; 16 bytes of 8-bit x serve
+// both), or, for groups of 32, one dword each of a chunk.
 //
 // Reading x costs as much as reading the codes: every workgroup reads all of
 // it, from L2, and a load instruction takes the same 16 cycles of the address
@@ -204,9 +206,17 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // the scales, which the four lane groups would otherwise each load (8.5 us
 // instead of 9.0 on that weight at M = 1).
 //
-// A product of one scale group starts at zero and is added into the fp32 sums with its scale, z taken off with the
-// sums of x (one more matrix product with a constant operand, shared by the T
-// row tiles).
+// A product of one scale group starts at zero and is added into the fp32 sums
+// with its scale, z taken off with the sums of x (one more matrix product with
+// a constant operand, shared by the T row tiles).
+//
+// Bound: memory and, right behind it, vector issue.  14336 x 4096, bf16, M = 1:
+// 30.8 MB in 8.4 us a call (3.7 TB/s; the DMA alone, with nothing computed,
+// takes 6.5-6.9); about 950 vector instructions a wave are 3.2 us of issue, 7
+// of 10 of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes
+// instead of 7 and takes 7.3 us; M = 16: INT8 8.7, E4M3 with grouped scales
+// 9.5, bf16 9.8 us.  4096 x 14336, bf16, M = 5: 10.8 us (two passes a wave, one
+// after the other).
 //
 // E4M3 activations are widened to bf16 as well: the FP8 matrix instruction
 // keeps too few bits of its sums (9e-5 off, relative, after 160 products,
@@ -271,7 +281,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   using P = Pass<A, GX, GS, T, MQ>;
   constexpr int SW = kPassSupers, XB = P::XB, XR = P::XR, NG = P::NG;
   constexpr int PER = 128 / GS;                       // scale groups of a super-chunk
-  constexpr bool PAIRS = A != Act::kBf16 && GS >= 64;
+  constexpr bool PAIRS = GS >= 64;
   constexpr int R = 16 * T;                           // rows of the workgroup
   static_assert(T <= 4, "one LDS array per tile");
   // One array per row tile: the compiler then knows which DMA a read depends
@@ -420,9 +430,9 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
     for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u) {
       const int p0 = 8 * XB * (u - v * SW / XR);  // first piece of super-chunk u
 #pragma unroll
-      for (int j = 0; j < 4; j += PAIRS ? 2 : 1) {
+      for (int j = 0; j < 4; j += PAIRS && XB == 1 ? 2 : 1) {
         if constexpr (A == Act::kBf16) {
-          xa[u][j] = xrow[(p0 + 4 * j + g) ^ nl];
+          xa[u][j] = xrow[(p0 + (PAIRS ? 4 * (j & 2) + 2 * g + (j & 1) : 4 * j + g)) ^ nl];
         } else if constexpr (PAIRS) {
           const u32x4 d = xrow[(p0 + 2 * j + g) ^ nl];
           xa[u][j] = Op::of(u32x2{d.x, d.y});
@@ -443,8 +453,8 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   };
 
   // The dwords of codes this lane feeds to the four matrix instructions of
-  // super-chunk u: instruction j takes dword g of chunk j, or, in pairs, dword
-  // 2 (g & 1) + j % 2 of chunk 2 (j / 2) + g / 2.
+  // super-chunk u: in pairs, instruction j takes dword 2 (g & 1) + j % 2 of
+  // chunk 2 (j / 2) + g / 2; otherwise dword g of chunk j.
   // (Byte 256 n + 16 (chunk ^ n) + 4 dword of the tile: u and j are constants,
   // so an address is one exclusive or; made anew for every pass, since kept
   // they would cost 16 registers.)

