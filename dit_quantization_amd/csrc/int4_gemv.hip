@@ -132,7 +132,8 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
   const int64_t rb = min(row0, N - 1);
   const __amdgpu_buffer_rsrc_t cbuf = make_buf(w.codes + rb * (K / 2), (uint32_t)(nrows * (K / 2)));
   const __amdgpu_buffer_rsrc_t sbuf = make_buf(w.scales + rb * G, (uint32_t)(nrows * G * 2));
-  const __amdgpu_buffer_rsrc_t zbuf = make_buf(w.zeros ? w.zeros + rb * G : nullptr, w.zeros ? (uint32_t)(nrows * G) : 0u);
+  const __amdgpu_buffer_rsrc_t zbuf = make_buf(w.zeros ? w.zeros + rb * G : nullptr,
+                                               w.zeros ? (uint32_t)(nrows * G) : 0u);
   const __amdgpu_buffer_rsrc_t xbuf = make_buf(x.x, (uint32_t)(K * (A == Act::kBf16 ? 2 : 1)));
   u32x4 cw[RW][CH];
   uint32_t sw[RW][CH], zw[RW][CH];
@@ -212,8 +213,8 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 //
 // Bound: memory and, right behind it, vector issue.  14336 x 4096, bf16, M = 1:
 // 30.8 MB in 8.4 us a call (3.7 TB/s; the DMA alone, with nothing computed,
-// takes 6.5-6.9); about 950 vector instructions a wave are 3.2 us of issue, 7
-// of 10 of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes
+// takes 6.5-6.9); about 900 vector instructions a wave are 3 us of issue, half
+// of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes
 // instead of 7 and takes 7.3 us; M = 16: INT8 8.7, E4M3 with grouped scales
 // 9.5, bf16 9.8 us.  4096 x 14336, bf16, M = 5: 10.8 us (two passes a wave, one
 // after the other).
@@ -226,8 +227,8 @@ struct Mfma {
   using Acc = f32x4;
   using X = u32x4;   // 8 bf16
   static __device__ __forceinline__ Acc mul(X x, X w, Acc c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0, 0,
-                                                   0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, w), c, 0,
+                                                   0, 0);
   }
   static __device__ __forceinline__ X unpack(uint32_t w) {
     const uint32_t lo = w & kNibbles, hi = (w >> 4) & kNibbles;
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   // codes, so that what comes first is waited for first.  x comes 4 rows x 256
   // contiguous bytes an instruction; DMA instruction u of tile t fills LDS
   // slots [64 u, 64 u + 64): lane l -> row r = 4 u + l / 16, slot j = l % 16,
-  // holding chunk 4 s0 + (j ^ r).  
+  // holding chunk 4 s0 + (j ^ r).
   const auto load = [&](P& p, int s0) {
     const int g0 = s0 * PER;  // first scale group of the pass
     if (wide && s0 + SW <= send) {

@@ -4,7 +4,7 @@
 // 64 or 128 is 4, 8 or 16 neighbouring lanes, so its range is a few lane
 // exchanges.  A wave takes runs of 64 vectors of one row; where rows end on a
 // group (the usual case) the whole tensor is one such row.  14336 x 4096: fp32
-// quantize 266 MB in 47 us (5.7 TB/s), bf16 148 MB in 32.6 (4.5); dequant to
+// quantize 266 MB in 47 us (5.7 TB/s), bf16 148 MB in 30.4 (4.9); dequant to
 // bf16 148 MB in 23 us with the codes in the last-level cache, 32 without (4.6).
 #include "device_common.hpp"
 #include "int4_kernels.hpp"
@@ -12,15 +12,14 @@
 
 namespace nvfp4 {
 
-// Runs of 64 vectors that a wave keeps in flight, and whether inputs are read
-// non-temporally, from a sweep over both (us, weights read again after 3 others
-// / after 14):
-//   quantize 14336 x 4096 fp32: 1 run 47.1 / 47.1; 2 runs 48.5 / 48.6; 1 run
-//   non-temporal 49.9 / 51.3.  bf16: 2 runs non-temporal 32.6 / 33.3, 1 run 38;
-//   1024 x 4096 bf16: 2 runs non-temporal 4.3, temporal 4.8, 4 runs 5.2.
-//   dequant 14336 x 4096 to bf16: 4 runs 23.2 / 32.3, 2 runs 22.9 / 33.4; 4 runs
-//   non-temporal 32.8 / 32.7; to fp32: 2 runs 37.0 / 54.8, 4 runs 39.3 / 55.4.
-constexpr int kQuantizeRunsF32 = 1, kQuantizeRunsBf16 = 2, kDequantRunsF32 = 2, kDequantRunsBf16 = 4;
+// Runs of 64 vectors that a wave keeps in flight, from a sweep over 1, 2, 4
+// and 8 (us, weights read again after 3 others / after 14): quantize 14336 x
+// 4096 fp32 46.9 / 46.8 with 1, 48.6 / 48.4 with 2; bf16 30.3 / 30.7 with 2, 35.4
+// / 35.5 with 1; dequant to bf16 22.4 / 31.0 with 2, 24.8 / 36.8 with 1; to fp32
+// 37.4 / 54.4 and 42.6 / 65.6.  4 runs gain nothing on large weights and lose on
+// small ones.  (Inputs read non-temporally: fp32 49.6, bf16 30.5 and at 4096 x
+// 4096 11.6 instead of 10.6, dequant 31.4.)
+constexpr int runs_in_flight(bool quantize, bool bf16) { return quantize && !bf16 ? 1 : 2; }
 
 // The rows a launch sees: the tensor's own, or one of all its elements.
 struct RowView {
@@ -44,12 +43,8 @@ struct Raw {
   u32x4 a[BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const void* x, int64_t vec) {
     const u32x4* p = reinterpret_cast<const u32x4*>(x) + (BF16 ? vec : 2 * vec);
-    if (BF16) {
-      a[0] = __builtin_nontemporal_load(p);
-    } else {
-      a[0] = p[0];
-      a[BF16 ? 0 : 1] = p[1];
-    }
+    a[0] = p[0];
+    if (!BF16) a[BF16 ? 0 : 1] = p[1];
   }
   __device__ __forceinline__ void zero() {
     a[0] = u32x4{0, 0, 0, 0};
@@ -84,11 +79,11 @@ __device__ __forceinline__ float nearest_f32(float w, float s, float t) {
 }
 
 template <bool BF16, int RUNS>
-__global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restrict__ x, RowView rv, int L, int64_t G,
-                                                            uint8_t* __restrict__ codes,
+__global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restrict__ x, RowView rv, int shift,
+                                                            int64_t G, uint8_t* __restrict__ codes,
                                                             uint16_t* __restrict__ scales,
                                                             uint8_t* __restrict__ zeros) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, L = 1 << shift;  // vectors of a group
   const int64_t n_units = rv.rows * rv.units;
   for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < n_units;
        u += (int64_t)gridDim.x * 4) {
@@ -155,7 +150,7 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
       if (v < rv.nv) {
         reinterpret_cast<uint32_t*>(codes)[row * rv.nv + v] = word;
         if ((lane & (L - 1)) == 0) {
-          const int64_t slot = row * G + v / L;
+          const int64_t slot = row * G + (v >> shift);
           scales[slot] = (uint16_t)sb;
           if (zeros) zeros[slot] = (uint8_t)(uint32_t)z;
         }
@@ -169,7 +164,7 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const void* __restri
 template <bool BF16, int RUNS>
 __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __restrict__ codes,
                                                            const uint16_t* __restrict__ scales,
-                                                           const uint8_t* __restrict__ zeros, RowView rv, int L,
+                                                           const uint8_t* __restrict__ zeros, RowView rv, int shift,
                                                            int64_t G, void* __restrict__ out) {
   constexpr int HALVES = BF16 ? 1 : 2;
   const int lane = threadIdx.x & 63;
@@ -182,7 +177,7 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
       const int64_t v = min(v0 + 64 * k, rv.nv - 1);
-      const int64_t slot = row * G + v / L;
+      const int64_t slot = row * G + (v >> shift);
       w[k] = reinterpret_cast<const uint32_t*>(codes)[(row * rv.nv + v) / HALVES];
       sb[k] = scales[slot];
       z[k] = zeros ? zeros[slot] : 8u;
@@ -199,8 +194,7 @@ __global__ __launch_bounds__(256) void int4_dequant_kernel(const uint8_t* __rest
       u32x4 o;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[j] = BF16 ? f32_to_bf16_bits(f[BF16 ? 2 * j : 0]) | (f32_to_bf16_bits(f[BF16 ? 2 * j + 1 : 0]) << 16)
-                    : __float_as_uint(f[j]);
+        o[j] = BF16 ? pk_bf16(f[BF16 ? 2 * j : 0], f[BF16 ? 2 * j + 1 : 0]) : __float_as_uint(f[j]);
       __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(out) + row * rv.nv + v);
     }
   }
@@ -213,27 +207,26 @@ static dim3 stream_grid(const RowView& v) {
 
 hipError_t launch_int4_quantize(const void* x, bool bf16, int64_t rows, int64_t cols, int group, uint8_t* codes,
                                 uint16_t* scales, uint8_t* zeros, hipStream_t stream) {
-  const RowView v = row_view(rows, cols, group, 8, bf16 ? kQuantizeRunsBf16 : kQuantizeRunsF32);
+  const RowView v = row_view(rows, cols, group, 8, runs_in_flight(true, bf16));
   const int64_t G = (cols + group - 1) / group;
-#define INT4_QUANTIZE(B, R)                                                                                        \
-  hipLaunchKernelGGL((int4_quantize_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, x, v, group / 8, G, codes, \
-                     scales, zeros)
-  if (bf16) INT4_QUANTIZE(true, kQuantizeRunsBf16);
-  else INT4_QUANTIZE(false, kQuantizeRunsF32);
+#define INT4_QUANTIZE(B)                                                                                        \
+  hipLaunchKernelGGL((int4_quantize_kernel<B, runs_in_flight(true, B)>), stream_grid(v), dim3(256), 0, stream, x, \
+                     v, __builtin_ctz(group / 8), G, codes, scales, zeros)
+  if (bf16) INT4_QUANTIZE(true);
+  else INT4_QUANTIZE(false);
 #undef INT4_QUANTIZE
   return hipGetLastError();
 }
 
 hipError_t launch_int4_dequant(const Int4Weight& w, int64_t rows, int64_t cols, void* out, bool bf16_out,
                                hipStream_t stream) {
-  const RowView v = bf16_out ? row_view(rows, cols, w.group, 8, kDequantRunsBf16)
-                             : row_view(rows, cols, w.group, 4, kDequantRunsF32);
+  const RowView v = row_view(rows, cols, w.group, bf16_out ? 8 : 4, runs_in_flight(false, bf16_out));
   const int64_t G = (cols + w.group - 1) / w.group;
-#define INT4_DEQUANT(B, R)                                                                                             \
-  hipLaunchKernelGGL((int4_dequant_kernel<B, R>), stream_grid(v), dim3(256), 0, stream, w.codes, w.scales, w.zeros, v, \
-                     w.group / (B ? 8 : 4), G, out)
-  if (bf16_out) INT4_DEQUANT(true, kDequantRunsBf16);
-  else INT4_DEQUANT(false, kDequantRunsF32);
+#define INT4_DEQUANT(B)                                                                                            \
+  hipLaunchKernelGGL((int4_dequant_kernel<B, runs_in_flight(false, B)>), stream_grid(v), dim3(256), 0, stream,     \
+                     w.codes, w.scales, w.zeros, v, __builtin_ctz(w.group / (B ? 8 : 4)), G, out)
+  if (bf16_out) INT4_DEQUANT(true);
+  else INT4_DEQUANT(false);
 #undef INT4_DEQUANT
   return hipGetLastError();
 }

@@ -1,5 +1,5 @@
-// Reductions over neighbouring lanes with DPP moves (no LDS round trip), used
-// by the group-scaled 4-bit and 8-bit kernels.
+// Reductions over neighbouring lanes with DPP moves (no LDS round trip), and
+// conversion to bf16 pairs, used by the group-scaled 4-bit and 8-bit kernels.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -48,6 +48,15 @@ __device__ __forceinline__ T lanes_all(T v, int L, F f) {
   if (L >= 8) v = f(v, dpp<kDppHalfMirror>(v));
   if (L >= 16) v = f(v, dpp<kDppMirror>(v));
   return v;
+}
+
+typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
+typedef float f32_pair __attribute__((ext_vector_type(2)));
+
+// Two floats to nearest even bf16, the first in the low half (one instruction;
+// the shifts and masks of f32_to_bf16_bits are five an element).
+__device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32_pair{lo, hi}), bf16_pair));
 }
 
 }  // namespace nvfp4

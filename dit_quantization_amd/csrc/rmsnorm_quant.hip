@@ -15,9 +15,9 @@
 // codes; only a wave that has such an element redoes its vectors in fp64.
 //
 // Bound by memory at long rows (4096 x 4096, bf16 with a bf16 residual, E4M3 in
-// groups of 128: 118 MB in 24.5 us, 4.8 TB/s; a large copy runs at 5.1), with
-// vector issue close behind (16 instructions an element in that form, 22 in the
-// all-fp64 one); 110593 x 128 to INT8: 43 MB in 9.9 us.
+// groups of 128: 118 MB in 23.5 us, 5.0 TB/s; a large copy runs at 5.1), with
+// vector issue behind it (34 instructions an element there are 15 us, 22 with
+// one INT8 scale a row); 110593 x 128 to INT8: 43 MB in 9.9 us.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -78,7 +78,7 @@ struct Vec8 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (!BF16) a[BF16 ? 0 : j / 4][j % 4] = __float_as_uint(v[j]);
-      else if (j & 1) a[0][j / 2] = f32_to_bf16_bits(v[j - 1]) | (f32_to_bf16_bits(v[j]) << 16);
+      else if (j & 1) a[0][j / 2] = pk_bf16(v[j - 1], v[j]);
     }
   }
 };
@@ -154,7 +154,8 @@ __device__ __forceinline__ float fresh(float v) {
 }
 
 template <int T, int V, bool XBF, Res RES, bool WBF>
-__global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1) void rmsnorm_quant_kernel(NormArgs a, double inv_cols, double inv_top) {
+__global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1) void rmsnorm_quant_kernel(
+    NormArgs a, double inv_cols, double inv_top) {
   constexpr int B = T < 256 ? 256 : T, TEAMS = B / T, NW = T / 64;
   const int t = threadIdx.x % T;
   const int64_t r = (int64_t)blockIdx.x * TEAMS + threadIdx.x / T;
@@ -162,18 +163,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
   const bool live_row = r < a.rows;
   // Where a thread has many vectors the weight, and then h too, is read again
   // for the codes (a cache hit; the registers are worth more: two workgroups
-  // of 1024 threads a CU instead of one take 2000 x 14336 from 50 to 43 us).
-  constexpr bool kKeep = V <= (T == 1024 ? 1 : 2), kKeepH = V <= 4;
+  // of 1024 threads a CU instead of one take 2000 x 14336 from 50 to 43 us, 400
+  // x 28672 in bf16 from 21.9 to 20.5; in fp32, twice the bytes, keeping h is
+  // faster there, 38.7 to 42.2).
   constexpr bool HBF = RES == Res::kNone ? XBF : RES == Res::kBf16;
+  constexpr bool kKeep = V <= (T == 1024 ? 1 : 2), kKeepH = V <= (HBF ? 2 : 4);
   constexpr bool kFast = HBF && WBF;
   using Max = typename std::conditional<kFast, float, double>::type;
   Vec8<HBF> h[kKeepH ? V : 1];
   Vec8<WBF> w[kKeep ? V : 1];
   double ss = 0.0;
-  Max m[V];
+  // Maximum |h w| of each vector; where h is not kept one for all of them, and
+  // the groups' are taken again.
+  constexpr int kUnroll = kKeepH ? V : 1;
+  Max m[kUnroll] = {};
+  const auto top_of = [](const Vec8<HBF>& hv, const Vec8<WBF>& wv, Max top) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (kFast) top = fmaxf(top, fabsf(hv.at(j) * wv.at(j)));
+      else top = fmax(top, fabs((double)hv.at(j) * (double)wv.at(j)));
+    }
+    return top;
+  };
   __shared__ double red_ss[16];
   __shared__ Max red_max[16];
-#pragma unroll
+#pragma unroll kUnroll
   for (int v = 0; v < V; ++v) {
     const int i = t + T * v;
     Vec8<WBF>& wv = w[kKeep ? v : 0];
@@ -195,14 +209,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
       }
       load_weight<WBF>(a, 8 * i, wv);
     }
-    m[v] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double d = (double)hv.at(j);
-      ss = __builtin_fma(d, d, ss);
-      if constexpr (kFast) m[v] = fmaxf(m[v], fabsf(hv.at(j) * wv.at(j)));
-      else m[v] = fmax(m[v], fabs(d * (double)wv.at(j)));
-    }
+    for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)hv.at(j), (double)hv.at(j), ss);
+    m[v % kUnroll] = top_of(hv, wv, m[v % kUnroll]);
     if (V > 2) __builtin_amdgcn_sched_barrier(0);  // one vector's operands at a time
   }
   const auto add = [](double p, double q) { return p + q; };
@@ -210,14 +219,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
   Max all = 0;  // the row's maximum
   if (a.group == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) all = most(all, m[v]);
+    for (int v = 0; v < kUnroll; ++v) all = most(all, m[v]);
   }
   constexpr int W = T < 64 ? T : 64;
   ss = lanes_all<W>(ss, add);
   if (a.group == 0) all = lanes_all<W>(all, most);
-  if (T > 64) {
-    // 4 (16) waves: every lane reads the partial results, which the lanes of
-    // a quad (of a run of 16) then combine in the same way everywhere
+  if constexpr (T > 64) {
+    // every lane reads the partial results, which each run of 4, 8 or 16 lanes
+    // (as many as waves) then combines in the same way
     const int wave = threadIdx.x / 64;
     if (threadIdx.x % 64 == 0) {
       red_ss[wave] = ss;
@@ -225,15 +234,15 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
     }
     __syncthreads();
     ss = red_ss[threadIdx.x % NW];
-    ss = NW == 4 ? lanes_all<4>(ss, add) : lanes_all<16>(ss, add);
+    ss = lanes_all<NW>(ss, add);
     if (a.group == 0) {
       all = red_max[threadIdx.x % NW];
-      all = NW == 4 ? lanes_all<4>(all, most) : lanes_all<16>(all, most);
+      all = lanes_all<NW>(all, most);
     }
   }
   const double ms = __builtin_fma(ss, inv_cols, a.eps);
   const double inv = ms > 0.0 ? rsqrt64(ms) : 0.0;
-  const int L = a.group / 8, G = a.group ? (a.cols + a.group - 1) / a.group : 1;
+  const int L = a.group / 8, Ls = 31 - __builtin_clz(L | 1), G = a.group ? (a.cols + a.group - 1) / a.group : 1;
   // scale, and the factor that turns h w into y / s
   const auto scale_of = [&](Max top, float& s) {
     s = (float)((double)top * inv * inv_top);
@@ -246,24 +255,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
     k = scale_of(all, s_row);
     if (t == 0 && live_row) a.scales[r] = s_row;
   }
-#pragma unroll
+#pragma unroll kUnroll
   for (int v = 0; v < V; ++v) {
     const int i = t + T * v;
-    Max top = all;
-    float s = s_row;
-    if (a.group) {
-      top = lanes_all(m[v], L, most);
-      k = scale_of(top, s);
-      if (live_row && i < n8 && (i & (L - 1)) == 0) a.scales[r * G + i / L] = s;
+    const bool live = live_row && i < n8;
+    Vec8<WBF>& wv = w[kKeep ? v : 0];
+    Vec8<HBF>& hv = h[kKeepH ? v : 0];
+    if constexpr (!kKeepH) {
+      hv.zero();
+      wv.zero();
     }
-    if (live_row && i < n8) {
-      Vec8<WBF>& wv = w[kKeep ? v : 0];
+    if (live) {
       if (!kKeep) load_weight<WBF>(a, 8 * i, wv);
-      Vec8<HBF>& hv = h[kKeepH ? v : 0];
       if constexpr (!kKeepH) {
         if constexpr (RES == Res::kNone) hv.load(a.x, r * a.x_stride + 8 * i);
         else hv.load(a.residual_out, r * a.cols + 8 * i);
       }
+    }
+    Max top = all;
+    float s = s_row;
+    if (a.group) {
+      top = lanes_all(kKeepH ? m[v % kUnroll] : top_of(hv, wv, 0), L, most);
+      k = scale_of(top, s);
+      if (live && (i & (L - 1)) == 0) a.scales[r * G + (i >> Ls)] = s;
+    }
+    if (live) {
       u32x2 q;
       bool exact = true;
       if constexpr (kFast) {
@@ -298,8 +314,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T == 1024 ? (V <= 2 ? 8 : 4) : 1
 
 // Threads a row and vectors a thread, by the row's length, from a sweep over
 // both: the fewest vectors a thread without teams that are mostly idle.  (us:
-// 4096 x 4096, 256 x 2 25.4, 1024 x 1 28.1, 256 x 4 28.5; 2048 x 8192, 1024 x 1
-// 26.7, 256 x 4 30.5; 16384 x 1024, 64 x 2 25.4, 256 x 1 30.8.)
+// 4096 x 4096, 512 x 1 25.2, 256 x 2 25.7, 1024 x 1 27.5, 256 x 4 29.6; 300 x 4096,
+// 512 x 1 4.3, 256 x 2 4.6, 1024 x 1 4.9; 2048 x 8192, 1024 x 1 26.3, 512 x 2 28.0;
+// 2000 x 14336, 1024 x 2 43.7, 512 x 4 46.6; 16384 x 1024, 64 x 2 24.8, 256 x 1
+// 29.3.)
 template <bool XBF, Res RES, bool WBF>
 hipError_t launch_norm(const NormArgs& all, hipStream_t stream) {
   const int n8 = all.cols / 8, G = all.group ? (all.cols + all.group - 1) / all.group : 1;
@@ -325,7 +343,7 @@ hipError_t launch_norm(const NormArgs& all, hipStream_t stream) {
     else if (n8 <= 64) NORM_CASE(64, 1);
     else if (n8 <= 128) NORM_CASE(64, 2);
     else if (n8 <= 256) NORM_CASE(256, 1);
-    else if (n8 <= 512) NORM_CASE(256, 2);
+    else if (n8 <= 512) NORM_CASE(512, 1);
     else if (n8 <= 1024) NORM_CASE(1024, 1);
     else if (n8 <= 2048) NORM_CASE(1024, 2);
     else if (n8 <= 4096) NORM_CASE(1024, 4);

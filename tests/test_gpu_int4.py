@@ -377,6 +377,26 @@ def test_norm_strides_in_place_and_guards():
         int4.rmsnorm_quant8(torch.zeros((1, 16), dtype=BF, device=DEV).expand(4, 16))
 
 
+@pytest.mark.parametrize("cols", [256, 4096, 16400, 40016])
+def test_norm_sums_in_bf16(cols):
+    """Sums that end half way between bf16 values, below its normal range and
+    next to its largest value, written onto the residual."""
+    g = rng(cols)
+    x = g.standard_normal((4, cols)).astype(np.float32)
+    r = g.standard_normal((4, cols)).astype(np.float32)
+    x[0] = g.integers(128, 256, cols)                # + 1/2: half way
+    r[0] = g.choice([-0.5, 0.5], cols)
+    x[1], r[1] = x[1] * 2.0 ** -130, r[1] * 2.0 ** -131
+    x[2], r[2] = 2.0 ** 127, (2.0 ** 126 - 2.0 ** 119) * g.choice([1, -1], cols)
+    w = tensor(np.ones(cols), BF)
+    for group, dtype in ((0, torch.int8), (128, torch.float8_e4m3fn)):
+        rt = tensor(r, BF)
+        out = (torch.empty((4, cols), dtype=dtype, device=DEV),
+               torch.empty((4, -(-cols // group) if group else 1), dtype=torch.float32, device=DEV), rt)
+        got = check_norm(tensor(x, BF), rt, w, 0.0, group, dtype, out=out)
+        assert got[2] is rt
+
+
 def test_norm_of_more_rows_than_one_launch_takes():
     """2^24 + 5 rows of 16 columns: the rows of either launch as if alone."""
     rows = (1 << 24) + 5
