@@ -208,16 +208,18 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // instead of 9.0 on that weight at M = 1).
 //
 // A product of one scale group starts at zero and is added into the fp32 sums
-// with its scale, z taken off with the sums of x (one more matrix product with
-// a constant operand, shared by the T row tiles).
+// with its scale.  The zero points are taken off with the sums of x over the
+// groups (a matrix product with a constant operand, shared by the T row tiles)
+// times s z, in fp32 matrix instructions of 4 groups (4096 x 14336, M = 1, groups
+// of 128: bf16 9.0 us, INT8 7.4; with multiply-adds of every group 9.5 and 7.9).
 //
 // Bound: memory and, right behind it, vector issue.  14336 x 4096, bf16, M = 1:
-// 30.8 MB in 8.4 us a call (3.7 TB/s; the DMA alone, with nothing computed,
-// takes 6.5-6.9); about 900 vector instructions a wave are 3 us of issue, half
-// of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes
-// instead of 7 and takes 7.3 us; M = 16: INT8 8.7, E4M3 with grouped scales
-// 9.5, bf16 9.8 us.  4096 x 14336, bf16, M = 5: 10.8 us (two passes a wave, one
-// after the other).
+// 30.8 MB in 8.2 us a call (3.8 TB/s; the DMA alone, with nothing computed,
+// takes 6.5-6.9); about 850 vector instructions a wave are 2.8 us of issue, half
+// of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes instead
+// of 7 and takes 7.4 us; M = 16: INT8 8.7, E4M3 with grouped scales 9.4, bf16
+// 9.7 us.  4096 x 14336, bf16: M = 1 9.1, M = 5 10.6, M = 16 13.3 us; a workgroup
+// takes 8 us even where only a quarter of the CUs have one, reading x among it.
 //
 // E4M3 activations are widened to bf16 as well: the FP8 matrix instruction
 // keeps too few bits of its sums (9e-5 off, relative, after 160 products,
@@ -291,7 +293,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   // 9.8 us instead of 9.2).
   __shared__ u32x4 lds_c0[NW][256], lds_c1[NW][256], lds_c2[NW][256], lds_c3[NW][256];
   __shared__ u32x4 lds_x[NW][256];
-  __shared__ __align__(16) uint32_t lds_s[NW][T == 1 ? 28 * NG : 4];
+  __shared__ __align__(16) uint32_t lds_s[NW][T == 1 ? (GX ? 28 : 12) * NG : 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const auto tile = [&](int t) {  // t is a constant once the loops are unrolled
     return t == 0 ? lds_c0[wave] : t == 1 ? lds_c1[wave] : t == 2 ? lds_c2[wave] : lds_c3[wave];
@@ -417,8 +419,9 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   // x of round v through LDS into the operands' layout: piece p (16 bytes) of
   // row r lies in slot p ^ r of the row, so neither side has bank conflicts.
   // Rows past 4 MQ are not written; what is read there only reaches sums of
-  // rows past M.  Fills xa for the round's super-chunks and their sums of x.
-  const auto spread = [&](const P& p, int v, typename Op::X (&xa)[SW][4], f32x4 (&xs)[NG]) {
+  // rows past M.  Fills xa for the round's super-chunks and xs with the sums of
+  // x over their scale groups, for row nl of x.
+  const auto spread = [&](const P& p, int v, typename Op::X (&xa)[SW][4], float (&xs)[NG]) {
     wave_fence();
 #pragma unroll
     for (int q = 0; q < MQ; ++q) {
@@ -446,9 +449,8 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
       for (int q = 0; q < PER; ++q) {
         Acc c = {};
 #pragma unroll
-        for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::ones(), c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xs[u * PER + q][i] = (float)c[i];
+        for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(Op::ones(), xa[u][j], c);
+        xs[u * PER + q] = (float)c[0];
       }
     }
   };
@@ -495,30 +497,49 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
     wave_fence();
   };
 
+  // Takes the zero points of tile t off: sum_g x_sum[m, g] (s z)[n, g], an fp32
+  // matrix product of 4 groups an instruction, of which this lane feeds group
+  // 4 a + g (s z is exact: 8 and 4 significant bits).
+  const auto sums_of = [&](const float (&xs)[NG], float (&xz)[NG / 4]) {
+#pragma unroll
+    for (int a = 0; a < NG / 4; ++a) {
+      const float even = g == 2 ? xs[4 * a + 2] : xs[4 * a], odd = g == 3 ? xs[4 * a + 3] : xs[4 * a + 1];
+      xz[a] = -(g & 1 ? odd : even);
+      if constexpr (GX) xz[a] *= st_f[16 * (4 * a + g) + nl];
+    }
+  };
+  const auto take_zeros = [&](int t, const float (&xz)[NG / 4]) {
+#pragma unroll
+    for (int a = 0; a < NG / 4; ++a) {
+      const int at = 4 * (a * R + 16 * t + nl) + g;
+      const float s = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(st_s)[at]);
+      const float z = (float)reinterpret_cast<const uint8_t*>(st_z)[at];
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xz[a], s * z, acc[t], 0, 0, 0);
+    }
+  };
+
   // Products of super-chunk u of tile t.
-  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
+  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4]) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int at = u * PER + q;
       const u32x2 s4 = reinterpret_cast<const u32x2*>(st_s)[at / 4 * R + 16 * t + nl];
-      const uint32_t z4 = st_z[at / 4 * R + 16 * t + nl];
       Acc c = {};
 #pragma unroll
       for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(d[j]), c);
       const uint32_t s2 = at & 2 ? s4.y : s4.x;
       const float s = __uint_as_float(at & 1 ? s2 & 0xFFFF0000u : s2 << 16);
-      const float z = (float)((z4 >> (8 * (at & 3))) & 0xFFu);
       f32x4 f = f32x4{s, s, s, s};
       if constexpr (GX) f *= *reinterpret_cast<const f32x4*>(&st_f[16 * at + 4 * g]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        acc[t][i] = __builtin_fmaf(__builtin_fmaf(-z, xs[at][i], (float)c[i]), f[i], acc[t][i]);
+        acc[t][i] = __builtin_fmaf((float)c[i], f[i], acc[t][i]);
     }
   };
 
   const auto compute = [&](const P& p) {
     typename Op::X xa[SW][4];
-    f32x4 xs[NG];
+    float xs[NG], xz[NG / 4];
     if constexpr (T == 1) {
       // round by round: few operands are live
       spread_scales(p);
@@ -527,14 +548,19 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
         spread(p, v, xa, xs);
 #pragma unroll
         for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u)
-          multiply(0, u, codes_of(0, u), xa, xs);
+          multiply(0, u, codes_of(0, u), xa);
       }
+      sums_of(xs, xz);
+      take_zeros(0, xz);
     } else {
       // tile by tile, in the order of the DMA, so that a tile's products
       // overlap the later tiles' DMA
 #pragma unroll
       for (int v = 0; v < XR; ++v) spread(p, v, xa, xs);
       spread_scales(p);
+      sums_of(xs, xz);
+#pragma unroll
+      for (int t = 0; t < T; ++t) take_zeros(t, xz);  // while the codes arrive
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         __builtin_amdgcn_sched_barrier(0);
@@ -542,7 +568,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
 #pragma unroll
         for (int u = 0; u < SW; ++u) cw[u] = codes_of(t, u);
 #pragma unroll
-        for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa, xs);
+        for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa);
       }
     }
   };
@@ -582,12 +608,12 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
 // Waves and rows per workgroup, from a sweep over N = 256..28672, K =
 // 512..14336 and M = 1..16 of the three types (us a call, back to back):
 //  * N <= 4096: 16 rows, so that up to 256 CUs have a workgroup each; 16 waves
-//    where K has more than one pass for each of 8 (4096 x 14336, bf16, M = 3:
-//    8.9 with 16, 9.7 with 8; 4096 x 4096: 5.3, 5.1);
-//  * N <= 8192: 32 rows for the same reason (8192 x 4096, INT8, M = 16: 6.4;
-//    16 rows 6.8, 64 rows 7.9);
+//    where K has more than one pass for each of 8 (4096 x 14336, bf16, M =
+//    16: 13.2 with 16, 14.7 with 8; 4096 x 4096: 6.0 with either);
+//  * N <= 8192: 32 rows for the same reason (8192 x 4096, INT8, M = 16: 6.5;
+//    16 rows 6.8, 64 rows 7.7);
 //  * above: 64 rows, x being read once per workgroup (14336 x 4096, INT8, M =
-//    16: 8.9; 32 rows 10.9, 16 rows 11.8).
+//    16: 8.7; 32 rows 10.7, 16 rows 11.7).
 template <Act A, bool GX>
 hipError_t launch_mfma(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, int G, void* y, int b,
                        hipStream_t stream) {
@@ -619,9 +645,9 @@ hipError_t launch_mfma(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t
 }
 
 // One row of few weights goes to the dot products, which start sooner (1024 x
-// 14336, bf16: 5.8 us, the matrix kernel 8.1; 4096 x 8192: 6.5, 7.2); a large
-// weight to the matrix kernel, which reads longer runs (4096 x 14336: 11.4,
-// 8.9; 14336 x 4096: 9.0, 8.5; 8192 x 8192: 9.9, 9.6).  K is split over 2 or 4 waves.
+// 14336, bf16: 4.8 us, the matrix kernel 7.7; 4096 x 8192: 6.4, 6.8); a large
+// weight to the matrix kernel, which reads longer runs (4096 x 14336: 11.4, 9.1;
+// 14336 x 4096: 9.0, 8.2; 8192 x 8192: 9.9, 9.3).  K is split over 2 or 4 waves.
 template <Act A>
 hipError_t launch_gemv(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, void* y, int b,
                        hipStream_t stream) {
