@@ -111,7 +111,8 @@ int int4_gemv_w4a8(const void* x, int x_dtype, const float* x_scales, int x_grou
  *   code    = nearest INT8 (ties to even) or E4M3 value to y / scale
  *   h is what the next layer's residual stream holds, and the norm is of its
  *   rounded value; y is never rounded to 16 bits: sums and quotients are
- *   held in fp64, so every code is decided by the definition above.
+ *   held in fp64, so every code is decided by the definition above.  (A
+ *   weight so large that a scale passes fp32's range is a caller error.)
  *   x        [rows, cols] of x_dtype (NVFP4_F32 or NVFP4_BF16), rows
  *            x_stride elements apart
  *   residual [rows, cols] of res_dtype (x_dtype or NVFP4_F32), rows

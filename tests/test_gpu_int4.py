@@ -235,6 +235,32 @@ def test_products_at_the_largest_k(kind, M):
     assert np.array_equal(f32(y).astype(np.float64), want)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M", [1, 3, 8, 16])
+def test_products_of_one_sign(kind, M):
+    """Activations of one sign, whose code and zero parts are far larger than
+    their difference, stay within the bound of the sums."""
+    for N, K, group in ((48, 8704, 32), (4200, 1056, 64), (8200, 544, 128)):
+        print(f"[case] one sign {kind} M={M} N={N} K={K} group={group}", flush=True)
+        hw, w = packed_weight(N, K, group, False, 51)
+        g = rng(52)
+        x = np.abs(g.standard_normal((M, K))) + 1
+        if kind == "bf16":
+            args = (tensor(x, BF),)
+            v = f32(args[0]).astype(np.float64)
+        else:
+            G, grouped = -(-K // group), group != 64
+            q = tensor(x * 25).to(torch.int8) if kind == "int8" else tensor(x * 60).to(torch.float8_e4m3fn)
+            sx = np.exp(g.standard_normal((M, G if grouped else 1))).astype(np.float32)
+            args = (q, torch.from_numpy(sx).to(DEV))
+            v = q.cpu().numpy().astype(np.float64) if kind == "int8" else e4m3_values(q)
+            v = v * (ref.per_element(sx, K, group) if grouped else sx)
+        ystar, a = ref.product(v, *hw, group)
+        err = np.abs(f32(call(kind, args, w, group, FL)) - ystar)
+        tau = ref.product_bound(a, K)
+        assert np.all(err <= tau), f"worst {np.max(err / tau)} of the bound"
+
+
 def test_products_write_only_their_outputs_and_repeat():
     """Odd sizes between guards, and the same bits on every call."""
     for kind in ("bf16", "int8", "e4m3"):
