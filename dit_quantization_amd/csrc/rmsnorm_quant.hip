@@ -10,9 +10,11 @@
 //
 // A code is the nearest to the exact y / s, so sums, products and quotients
 // are fp64 wherever fp32 would round: h^2 always, the rest where h or w is
-// fp32.  With bf16 h and w the products h w are exact in fp32, and y / s in
-// fp32 decides a code unless it is within its error of half way between two
-// codes; only a wave that has such an element redoes its vectors in fp64.
+// fp32.  With bf16 h and w the products h w are exact in fp32 unless they leave
+// its range, and y / s in fp32 decides a code unless it is within its error of
+// half way between two codes; only a wave that has such an element redoes its
+// vectors in fp64, and where a maximum |h w| is next to either end of fp32's
+// range (or 0, as it is where all products underflow) it is taken again in fp64.
 //
 // Bound by memory at long rows (4096 x 4096, bf16 with a bf16 residual, E4M3 in
 // groups of 128: 118 MB in 23.5 us, 5.0 TB/s; a large copy runs at 5.1), with
@@ -148,7 +150,8 @@ __device__ __forceinline__ u32x2 encode_i8_fast(const float p[8], float k, bool&
 }
 // A value the compiler takes for a new one, so that what is computed from it
 // is not kept from earlier.
-__device__ __forceinline__ float fresh(float v) {
+template <class T>
+__device__ __forceinline__ T fresh(T v) {
   asm volatile("" : "+v"(v));
   return v;
 }
@@ -185,6 +188,27 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1)
     }
     return top;
   };
+  // Where fp32 products serve: the maximum far from overflow, and so far above
+  // fp32's smallest that products which lose bits there are neither the maximum
+  // nor more than code 0.
+  const auto in_range = [](float top) { return top >= 0x1p-100f && top <= 0x1p126f; };
+  // Maximum |h w| of vector v in fp64, of h and the weight as they lie in
+  // memory: kept in registers for this rare path, they would cost two waves a
+  // SIMD.
+  const auto wide_top_of = [&](int v) {
+    const int i = fresh(t + T * v);
+    double top = 0.0;
+    if (live_row && i < n8) {
+      Vec8<HBF> hv;
+      Vec8<WBF> wv;
+      if constexpr (RES == Res::kNone) hv.load(a.x, r * a.x_stride + 8 * i);
+      else hv.load(a.residual_out, r * a.cols + 8 * i);
+      load_weight<WBF>(a, 8 * i, wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmax(top, fabs((double)hv.at(j) * (double)wv.at(j)));
+    }
+    return top;
+  };
   __shared__ double red_ss[16];
   __shared__ Max red_max[16];
 #pragma unroll kUnroll
@@ -215,7 +239,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1)
     if (V > 2) __builtin_amdgcn_sched_barrier(0);  // one vector's operands at a time
   }
   const auto add = [](double p, double q) { return p + q; };
-  const auto most = [](Max p, Max q) { return p > q ? p : q; };
+  const auto most = [](auto p, auto q) { return p > q ? p : q; };
   Max all = 0;  // the row's maximum
   if (a.group == 0) {
 #pragma unroll
@@ -244,15 +268,31 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1)
   const double inv = ms > 0.0 ? rsqrt64(ms) : 0.0;
   const int L = a.group / 8, Ls = 31 - __builtin_clz(L | 1), G = a.group ? (a.cols + a.group - 1) / a.group : 1;
   // scale, and the factor that turns h w into y / s
-  const auto scale_of = [&](Max top, float& s) {
-    s = (float)((double)top * inv * inv_top);
+  const auto scale_of = [&](double top, float& s) {
+    s = (float)(top * inv * inv_top);
     if (s == 0.0f) s = 1.0f;
     return inv * rcp64((double)s);
   };
   float s_row = 1.0f;
   double k = 0.0;
   if (a.group == 0) {
-    k = scale_of(all, s_row);
+    double top = (double)all;
+    if constexpr (kFast) {
+      // the same for all threads of the row (a maximum of fmaxf's, so never NaN)
+      if (!in_range(all)) {
+        top = 0.0;
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) top = most(top, wide_top_of(v));
+        top = lanes_all<W>(top, most);
+        if constexpr (T > 64) {  // a row is a workgroup
+          __syncthreads();       // red_ss has been read
+          if (threadIdx.x % 64 == 0) red_ss[threadIdx.x / 64] = top;
+          __syncthreads();
+          top = lanes_all<NW>(red_ss[threadIdx.x % NW], most);
+        }
+      }
+    }
+    k = scale_of(top, s_row);
     if (t == 0 && live_row) a.scales[r] = s_row;
   }
 #pragma unroll kUnroll
@@ -276,17 +316,20 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1)
     float s = s_row;
     if (a.group) {
       top = lanes_all(kKeepH ? m[v % kUnroll] : top_of(hv, wv, 0), L, most);
-      k = scale_of(top, s);
+      double wide = (double)top;
+      if constexpr (kFast) {
+        // the same for the L lanes of a group
+        if (!in_range(top)) wide = lanes_all(wide_top_of(v), L, most);
+      }
+      k = scale_of(wide, s);
       if (live && (i & (L - 1)) == 0) a.scales[r * G + (i >> Ls)] = s;
     }
     if (live) {
       u32x2 q;
       bool exact = true;
       if constexpr (kFast) {
-        // Where fp32 products serve: the maximum far from overflow, and so far
-        // above fp32's smallest that products which lose bits there have code
-        // 0 either way; s normal, so |u| stays below Q and half a step.
-        exact = !(top >= 0x1p-100f && top <= 0x1p126f && s >= 0x1p-120f);
+        // s normal, so |u| stays below Q and half a step
+        exact = !(in_range(top) && s >= 0x1p-120f);
         float p[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = hv.at(j) * wv.at(j);

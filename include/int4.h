@@ -110,9 +110,11 @@ int int4_gemv_w4a8(const void* x, int x_dtype, const float* x_scales, int x_grou
  *             Q = 127 (INT4_I8) or 448 (INT4_E4M3); 1.0 where that is 0
  *   code    = nearest INT8 (ties to even) or E4M3 value to y / scale
  *   h is what the next layer's residual stream holds, and the norm is of its
- *   rounded value; y is never rounded to 16 bits: sums and quotients are
- *   held in fp64, so every code is decided by the definition above.  (A
- *   weight so large that a scale passes fp32's range is a caller error.)
+ *   rounded value; y is never rounded to 16 bits: products, maxima, sums and
+ *   quotients are held in fp64 wherever fp32 would round, underflow or
+ *   overflow, so codes and scales are decided by the definition above (short
+ *   of quotients within 2^-45 of half way, which fp64 cannot tell from it).
+ *   (A weight so large that a scale passes fp32's range is a caller error.)
  *   x        [rows, cols] of x_dtype (NVFP4_F32 or NVFP4_BF16), rows
  *            x_stride elements apart
  *   residual [rows, cols] of res_dtype (x_dtype or NVFP4_F32), rows

@@ -556,3 +556,62 @@ def test_refusals():
                                         ctypes.c_void_p(side.cuda_stream))
     torch.cuda.synchronize()
     assert st == nv.ERR_CAPTURE and bool((y == 7).all())
+
+
+# ---- far values, exact sums, long loops
+
+def check_norm_nearest(x, r, wt, eps, group, dtype):
+    """check_norm for inputs whose quotients may lie closer to half way than
+    fp64 tells: with eps = 1e-6 and h far below it 1 / sqrt(eps) is 1000 to
+    within 2^-55, and y / scale can be a half to within 2^-55 too (110.5 +
+    2.5e-15 is one of these), where the order of two fp64 products decides.
+    A code then is a nearest one to within the error of either side.  That is
+    below 2^-45 of the quotient: at most 74 additions of squares (64 a thread
+    and 10 exchanges; numpy's pairwise sums fewer), of which the root halves the
+    effect, and fewer than 30 further roundings, each 2^-53: 67 x 2^-53 < 2^-46.
+    (A quotient further than that from half way has one nearest code, so all
+    codes of ordinary quotients are equal.)"""
+    xf, rf, wf = f32(x), None if r is None else f32(r), f32(wt)
+    q, s, h = int4.rmsnorm_quant8(x, wt, residual=r, eps=eps, group_size=group, out_dtype=dtype)
+    e4m3 = dtype == torch.float8_e4m3fn
+    rq, rs, rh = ref.rmsnorm_quant8(xf, wf, rf, r is not None, eps, group, e4m3)
+    assert np.array_equal(f32(s), rs), f"scales: {np.abs(f32(s) / rs - 1).max()}"
+    assert h is None if r is None else np.array_equal(f32(h), rh)
+    codes = e4m3_values(q) if e4m3 else q.cpu().numpy().astype(np.float64)
+    d = (xf if r is None else rh).astype(np.float64)
+    with np.errstate(divide="ignore"):
+        inv = 1 / np.sqrt((d * d).sum(1) / d.shape[1] + eps)
+    inv[~d.any(1)] = 0
+    v = d * wf * inv[:, None] / ref.per_element(rs, d.shape[1], group or d.shape[1])
+    off = np.abs(v - codes) > np.abs(v - rq) + 2 * 2.0 ** -45 * np.abs(v)
+    assert not off.any(), f"{off.sum()} of {off.size} codes are not nearest"
+
+
+NORM_EXTREMES = [16, 64, 256, 1040, 4096, 8208, 14336, 16400, 65536]
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.float8_e4m3fn], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("cols", NORM_EXTREMES)
+def test_norm_where_products_leave_fp32(cols, dtype):
+    """bf16 values and weights whose products pass fp32's range at either end
+    although the norm and its scale are ordinary: whole rows, and single groups
+    of a row beside ordinary ones."""
+    g = rng(cols)
+    sign = lambda: g.choice([1.0, -1.0], cols)  # noqa: E731
+    x = g.standard_normal((7, cols))
+    x[1] = 2.0 ** 127 * sign()                                # h w passes the largest value
+    x[2] = 2.0 ** 126 * g.uniform(0.5, 1.9, cols) * sign()
+    x[3] = 2.0 ** -70 * g.uniform(0.5, 2, cols) * sign()      # with a small weight: below the normal range
+    x[4] = 2.0 ** -120 * g.uniform(0.5, 2, cols) * sign()     # ... and below the smallest value
+    x[5] = 0
+    x[6, : cols // 2] *= 2.0 ** -100                          # some groups only
+    x[6, cols // 2] = 2.0 ** 127
+    r = np.zeros((7, cols))
+    r[2], r[3] = -x[2] / 2, x[3]
+    weights = [np.full(cols, 2.0), np.exp2(g.uniform(1, 60, cols)) * sign(), np.exp2(g.uniform(-75, -65, cols)),
+               np.where(np.arange(cols) % 128 < 64, 2.0 ** -80, 2.0 ** 40)]
+    for i, w in enumerate(weights):
+        for eps in (0.0, 1e-6):
+            for group in (0, 32, 64, 128):
+                print(f"[case] norm extremes {cols} weight {i} eps={eps} group={group} {dtype}", flush=True)
+                check_norm_nearest(tensor(x, BF), tensor(r, BF) if i % 2 else None, tensor(w, BF), eps, group, dtype)
