@@ -207,11 +207,15 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // the scales, which the four lane groups would otherwise each load (8.5 us
 // instead of 9.0 on that weight at M = 1).
 //
-// A product of one scale group starts at zero and is added into the fp32 sums
-// with its scale.  The zero points are taken off with the sums of x over the
-// groups (a matrix product with a constant operand, shared by the T row tiles)
-// times s z, in fp32 matrix instructions of 4 groups (4096 x 14336, M = 1, groups
-// of 128: bf16 9.0 us, INT8 7.4; with multiply-adds of every group 9.5 and 7.9).
+// A product of one scale group starts at zero, the zero point is taken off with
+// the sum of x over the group (a matrix product with a constant operand, shared
+// by the T row tiles), and the difference is added into the fp32 sums with its
+// scale.  The difference has to be formed inside the group, where INT8 sums are
+// whole numbers: s z sum x of several groups as one fp32 matrix product saves
+// the multiply-adds (4096 x 14336, M = 1, bf16: 8.7 us instead of 8.9; INT8 7.1,
+// 7.2; M = 16 13.1, 13.0) but makes the fp32 sums as large as the code part of
+// a pass (14336 x 4096, M = 16, x of one sign: relative error 2.3e-6 for bf16
+// and 1.2e-6 for INT8 instead of 3.4e-8 and 2.5e-8).
 //
 // Bound: memory and, right behind it, vector issue.  14336 x 4096, bf16, M = 1:
 // 30.8 MB in 8.2 us a call (3.8 TB/s; the DMA alone, with nothing computed,
@@ -421,7 +425,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   // Rows past 4 MQ are not written; what is read there only reaches sums of
   // rows past M.  Fills xa for the round's super-chunks and xs with the sums of
   // x over their scale groups, for row nl of x.
-  const auto spread = [&](const P& p, int v, typename Op::X (&xa)[SW][4], float (&xs)[NG]) {
+  const auto spread = [&](const P& p, int v, typename Op::X (&xa)[SW][4]) {
     wave_fence();
 #pragma unroll
     for (int q = 0; q < MQ; ++q) {
@@ -445,13 +449,19 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
           xa[u][j] = Op::of(reinterpret_cast<const u32x2*>(&xrow[(p0 + 2 * j + (g >> 1)) ^ nl])[g & 1]);
         }
       }
+    }
+  };
+
+  // Sums of x over the scale groups of super-chunk u, for the four rows of x
+  // that this lane has in an accumulator.
+  const auto sums_of = [&](int u, const typename Op::X (&xa)[SW][4], f32x4 (&xs)[NG]) {
 #pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        Acc c = {};
+    for (int q = 0; q < PER; ++q) {
+      Acc c = {};
 #pragma unroll
-        for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(Op::ones(), xa[u][j], c);
-        xs[u * PER + q] = (float)c[0];
-      }
+      for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::ones(), c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xs[u * PER + q][i] = (float)c[i];
     }
   };
 
@@ -497,70 +507,50 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
     wave_fence();
   };
 
-  // Takes the zero points of tile t off: sum_g x_sum[m, g] (s z)[n, g], an fp32
-  // matrix product of 4 groups an instruction, of which this lane feeds group
-  // 4 a + g (s z is exact: 8 and 4 significant bits).
-  const auto sums_of = [&](const float (&xs)[NG], float (&xz)[NG / 4]) {
-#pragma unroll
-    for (int a = 0; a < NG / 4; ++a) {
-      const float even = g == 2 ? xs[4 * a + 2] : xs[4 * a], odd = g == 3 ? xs[4 * a + 3] : xs[4 * a + 1];
-      xz[a] = -(g & 1 ? odd : even);
-      if constexpr (GX) xz[a] *= st_f[16 * (4 * a + g) + nl];
-    }
-  };
-  const auto take_zeros = [&](int t, const float (&xz)[NG / 4]) {
-#pragma unroll
-    for (int a = 0; a < NG / 4; ++a) {
-      const int at = 4 * (a * R + 16 * t + nl) + g;
-      const float s = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(st_s)[at]);
-      const float z = (float)reinterpret_cast<const uint8_t*>(st_z)[at];
-      acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(xz[a], s * z, acc[t], 0, 0, 0);
-    }
-  };
-
   // Products of super-chunk u of tile t.
-  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4]) {
+  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int at = u * PER + q;
       const u32x2 s4 = reinterpret_cast<const u32x2*>(st_s)[at / 4 * R + 16 * t + nl];
+      const uint32_t z4 = st_z[at / 4 * R + 16 * t + nl];
       Acc c = {};
 #pragma unroll
       for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(d[j]), c);
       const uint32_t s2 = at & 2 ? s4.y : s4.x;
       const float s = __uint_as_float(at & 1 ? s2 & 0xFFFF0000u : s2 << 16);
+      const float z = (float)((z4 >> (8 * (at & 3))) & 0xFFu);
       f32x4 f = f32x4{s, s, s, s};
       if constexpr (GX) f *= *reinterpret_cast<const f32x4*>(&st_f[16 * at + 4 * g]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        acc[t][i] = __builtin_fmaf((float)c[i], f[i], acc[t][i]);
+        acc[t][i] = __builtin_fmaf(__builtin_fmaf(-z, xs[at][i], (float)c[i]), f[i], acc[t][i]);
     }
   };
 
   const auto compute = [&](const P& p) {
     typename Op::X xa[SW][4];
-    float xs[NG], xz[NG / 4];
+    f32x4 xs[NG];
     if constexpr (T == 1) {
       // round by round: few operands are live
       spread_scales(p);
 #pragma unroll
       for (int v = 0; v < XR; ++v) {
-        spread(p, v, xa, xs);
+        spread(p, v, xa);
 #pragma unroll
-        for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u)
-          multiply(0, u, codes_of(0, u), xa);
+        for (int u = v * SW / XR; u < (v + 1) * SW / XR; ++u) {
+          sums_of(u, xa, xs);
+          multiply(0, u, codes_of(0, u), xa, xs);
+        }
       }
-      sums_of(xs, xz);
-      take_zeros(0, xz);
     } else {
       // tile by tile, in the order of the DMA, so that a tile's products
       // overlap the later tiles' DMA
 #pragma unroll
-      for (int v = 0; v < XR; ++v) spread(p, v, xa, xs);
-      spread_scales(p);
-      sums_of(xs, xz);
+      for (int v = 0; v < XR; ++v) spread(p, v, xa);
 #pragma unroll
-      for (int t = 0; t < T; ++t) take_zeros(t, xz);  // while the codes arrive
+      for (int u = 0; u < SW; ++u) sums_of(u, xa, xs);
+      spread_scales(p);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         __builtin_amdgcn_sched_barrier(0);
@@ -568,7 +558,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
 #pragma unroll
         for (int u = 0; u < SW; ++u) cw[u] = codes_of(t, u);
 #pragma unroll
-        for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa);
+        for (int u = 0; u < SW; ++u) multiply(t, u, cw[u], xa, xs);
       }
     }
   };

@@ -83,7 +83,11 @@ int int4_dequant(const uint8_t* codes, const void* scales, const uint8_t* zeros,
  *   (NVFP4_BF16 or NVFP4_F32), 4-byte aligned
  *   0 <= M <= 16; K % 32 == 0, 0 < K <= 2^24; N <= 2^28, otherwise
  *   NVFP4_ERR_UNSUPPORTED (K % 16 != 0: NVFP4_ERR_SHAPE).  fp32 accumulation
- *   in a fixed order (results are reproducible), RNE bf16 output.
+ *   in a fixed order (results are reproducible), RNE bf16 output.  A group's
+ *   sum is the difference of sum x code and z sum x, then scaled and added: the
+ *   fp32 result is off by at most
+ *     2^-24 (129 sum_k |x| s (code + z) + (K / 32 + 26) sum_r |t_r|)
+ *   with t_r the terms of the sum over runs of 32 elements.
  */
 int int4_gemv_w4a16(const void* x, const uint8_t* codes, const void* scales, const uint8_t* zeros, int group,
                     int64_t M, int64_t N, int64_t K, void* y, int y_dtype, void* stream);
@@ -94,7 +98,8 @@ int int4_gemv_w4a16(const void* x, const uint8_t* codes, const void* scales, con
  *   x_scales fp32 [M, 1] with x_group 0, or [M, G] with x_group == group;
  *            4-byte aligned (another x_group is NVFP4_ERR_UNSUPPORTED)
  *   y[m, n] = round(sum_g s[n, g] sx[m, g] sum_{k in g} x[m, k] (code - z))
- *   INT8 sums inside a group are exact integers; everything else is fp32.
+ *   INT8 sums inside a group are exact integers, which leaves only the second
+ *   part of the bound above; everything else is fp32.
  *   Arguments and limits otherwise as int4_gemv_w4a16.
  */
 int int4_gemv_w4a8(const void* x, int x_dtype, const float* x_scales, int x_group, const uint8_t* codes,

@@ -615,3 +615,72 @@ def test_norm_where_products_leave_fp32(cols, dtype):
             for group in (0, 32, 64, 128):
                 print(f"[case] norm extremes {cols} weight {i} eps={eps} group={group} {dtype}", flush=True)
                 check_norm_nearest(tensor(x, BF), tensor(r, BF) if i % 2 else None, tensor(w, BF), eps, group, dtype)
+
+
+def exact_product(kind, M, N, K, group, grouped, seed):
+    """Inputs whose differences code - zero are few and small while codes, zero
+    points and activations are not, and scales of 8 significant bits: each
+    group's sums of x code and of x are whole numbers below 2^24, and the sums
+    of s sx x (code - zero) are multiples of 2^-7 below 2^17 in any order, so
+    the product is exact wherever a group's difference is taken before its
+    scale.  (device arguments, weight, the product)"""
+    g = rng(seed)
+    G = -(-K // group)
+    zeros = g.integers(1, 15, (N, G)).astype(np.uint8)
+    d = np.where(g.random((N, K)) < min(0.1, 400 / K), g.choice([-1, 1], (N, K)), 0)
+    codes = (np.repeat(zeros, group, 1)[:, :K] + d).astype(np.uint8)
+    scales = g.integers(129, 256, (N, G)) / 128
+    x = (8 * g.integers(8, 16, (M, K)) if kind == "e4m3" else g.integers(64, 128, (M, K))).astype(np.float64)
+    w = (torch.from_numpy(ref.pack(codes)).to(DEV), tensor(scales, BF), torch.from_numpy(zeros).to(DEV))
+    v = x
+    if kind == "bf16":
+        args = (tensor(x, BF),)
+    else:
+        sx = g.integers(1, 3, (M, G if grouped else 1)).astype(np.float64)
+        args = (tensor(x).to(torch.int8 if kind == "int8" else torch.float8_e4m3fn), tensor(sx))
+        v = x * (ref.per_element(sx, K, group) if grouped else sx)
+    sd = ref.per_element(scales, K, group) * d
+    for m in range(M):                                       # sums of any runs of 32: all partial sums stay below 2^17
+        parts = np.abs((v[m] * sd[:64]).reshape(-1, K // 32, 32).sum(2)).sum(1)
+        assert parts.max() < 2.0 ** 17
+    return args, w, v @ sd.T
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M", [1, 3, 8, 16])
+def test_products_take_the_zero_point_off_inside_the_group(kind, M):
+    """The sums of x (code - zero) of a group are formed before they meet its
+    scale: exact here, however large the parts they are the difference of."""
+    for N, K, group, grouped in ((48, 4096, 128, True), (37, 8704, 32, False), (37, 4128, 64, True),
+                                 (4200, 1056, 64, False), (4200, 8704, 128, True), (8200, 544, 32, True),
+                                 (8200, 4608, 128, False)):
+        print(f"[case] exact {kind} M={M} N={N} K={K} group={group} grouped={grouped}", flush=True)
+        args, w, want = exact_product(kind, M, N, K, group, grouped, M + N + K)
+        y = f32(call(kind, args, w, group, FL)).astype(np.float64)
+        assert np.array_equal(y, want), f"{(y != want).sum()} of {y.size} differ, worst {np.abs(y - want).max()}"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M,N,K,group", [(1, 48, 8704, 32), (1, 5000, 4096, 128), (3, 40, 14336, 64),
+                                         (16, 4200, 1056, 64), (8, 8200, 4608, 128)])
+def test_products_stay_within_the_stated_bound(kind, M, N, K, group):
+    """The bound of include/int4.h, of which INT8 has only the part of the sums
+    over groups, for activations of both signs and of one."""
+    (codes, scales, zeros), w = packed_weight(N, K, group, False, 81)
+    for grouped in (False, True):
+        for one_sign in (False, True):
+            print(f"[case] bound {kind} M={M} N={N} K={K} group={group} {grouped} {one_sign}", flush=True)
+            args, v = activations(kind, M, K, group, grouped, 82)
+            if one_sign:
+                x = args[0].float().abs().clamp(max=127 if kind == "int8" else 3e38)
+                args = (x.to(args[0].dtype),) + args[1:]
+                v = f32(x).astype(np.float64)
+                if kind != "bf16":
+                    sx = f32(args[1]).astype(np.float64)
+                    v = v * (ref.per_element(sx, K, group) if grouped else sx)
+            y = f32(call(kind, args, w, group, FL)).astype(np.float64)
+            s, d = ref.per_element(scales, K, group), codes.astype(np.float64) - ref.per_element(zeros, K, group)
+            ystar, a = ref.product(v, codes, scales, zeros, group)
+            runs = np.stack([np.abs(((s * d) * v[m]).reshape(N, K // 32, 32).sum(2)).sum(1) for m in range(M)])
+            tau = 2.0 ** -24 * ((0 if kind == "int8" else 129) * a + (K / 32 + 26) * runs)
+            assert np.all(np.abs(y - ystar) <= tau), f"worst {np.max(np.abs(y - ystar) / tau)} of the bound"
