@@ -162,9 +162,10 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
   for (int r = 0; r < RW; ++r) {
     acc[r] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      acc[r] = __builtin_fmaf(dot_chunk<A>(xc[c], cw[r][c], (float)zw[r][c]),
-                              bf16_bits_to_f32(sw[r][c]) * xc[c].scale, acc[r]);
+    for (int c = 0; c < CH; ++c) {
+      const float d = dot_chunk<A>(xc[c], cw[r][c], (float)zw[r][c]), s = bf16_bits_to_f32(sw[r][c]);
+      acc[r] = A == Act::kBf16 ? __builtin_fmaf(d, s, acc[r]) : __builtin_fmaf(d * s, xc[c].scale, acc[r]);
+    }
     __builtin_amdgcn_sched_barrier(0);  // compute order = row order
   }
   const float tot = lane_sums<RW>(acc, lane);
@@ -508,7 +509,7 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   };
 
   // Products of super-chunk u of tile t.
-  const auto multiply = [&](int t, int u, u32x4 d, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
+  const auto multiply = [&](int t, int u, u32x4 w4, const typename Op::X (&xa)[SW][4], const f32x4 (&xs)[NG]) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int at = u * PER + q;
@@ -516,15 +517,19 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
       const uint32_t z4 = st_z[at / 4 * R + 16 * t + nl];
       Acc c = {};
 #pragma unroll
-      for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(d[j]), c);
+      for (int j = q * 4 / PER; j < (q + 1) * 4 / PER; ++j) c = Op::mul(xa[u][j], Op::unpack(w4[j]), c);
       const uint32_t s2 = at & 2 ? s4.y : s4.x;
       const float s = __uint_as_float(at & 1 ? s2 & 0xFFFF0000u : s2 << 16);
       const float z = (float)((z4 >> (8 * (at & 3))) & 0xFFu);
-      f32x4 f = f32x4{s, s, s, s};
-      if constexpr (GX) f *= *reinterpret_cast<const f32x4*>(&st_f[16 * at + 4 * g]);
+      // (d s) sx and not d (s sx): the product of the scales may leave fp32's
+      // range where the result does not
+      f32x4 sx;
+      if constexpr (GX) sx = *reinterpret_cast<const f32x4*>(&st_f[16 * at + 4 * g]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[t][i] = __builtin_fmaf(__builtin_fmaf(-z, xs[at][i], (float)c[i]), f[i], acc[t][i]);
+      for (int i = 0; i < 4; ++i) {
+        const float d = __builtin_fmaf(-z, xs[at][i], (float)c[i]);
+        acc[t][i] = GX ? __builtin_fmaf(d * s, sx[i], acc[t][i]) : __builtin_fmaf(d, s, acc[t][i]);
+      }
     }
   };
 

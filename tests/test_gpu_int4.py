@@ -684,3 +684,30 @@ def test_products_stay_within_the_stated_bound(kind, M, N, K, group):
             runs = np.stack([np.abs(((s * d) * v[m]).reshape(N, K // 32, 32).sum(2)).sum(1) for m in range(M)])
             tau = 2.0 ** -24 * ((0 if kind == "int8" else 129) * a + (K / 32 + 26) * runs)
             assert np.all(np.abs(y - ystar) <= tau), f"worst {np.max(np.abs(y - ystar) / tau)} of the bound"
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("M", [1, 5])
+def test_products_with_scales_far_apart(kind, M):
+    """Group scales whose product with the weight's leaves fp32's range though
+    the result does not: each sum is scaled by one and then by the other."""
+    N, K, group = 40, 4096, 128
+    g = rng(61)
+    G = K // group
+    codes = g.integers(0, 16, (N, K)).astype(np.uint8)
+    zeros = g.integers(0, 16, (N, G)).astype(np.uint8)
+    codes[0] = np.repeat(zeros[0], group)                    # a row of zeros
+    q = g.integers(1, 127, (M, K)) if kind == "int8" else 8 * g.integers(8, 16, (M, K))
+    x = tensor(q).to(torch.int8 if kind == "int8" else torch.float8_e4m3fn)
+    s0 = ref.bf16(g.uniform(1, 2, (N, G)).astype(np.float32))
+    x0 = g.uniform(1, 2, (M, G)).astype(np.float32)
+    packed, z = torch.from_numpy(ref.pack(codes)).to(DEV), torch.from_numpy(zeros).to(DEV)
+    s, sx = (s0 * np.float32(2.0 ** -72)), (x0 * np.float32(2.0 ** -73))
+    y = f32(int4.gemv_w4a8(x, tensor(sx), packed, tensor(s, BF), z, out_dtype=FL)).astype(np.float64)
+    ystar, a = ref.product(q * ref.per_element(sx, K, group), codes, s, zeros, group)
+    # each of the sum's operations may also round at 2^-149, fp32's last step
+    assert np.all(np.abs(y - ystar) <= ref.product_bound(a, K) + (160 + K / 32) * 2.0 ** -149)
+    assert np.abs(ystar[:, 1:]).max() > 2.0 ** -126 and not y[:, 0].any()
+    s, sx = (s0 * np.float32(2.0 ** 10)), (x0 * np.float32(2.0 ** 120))
+    y = f32(int4.gemv_w4a8(x, tensor(sx), packed, tensor(s, BF), z, out_dtype=FL))
+    assert not y[:, 0].any()                                 # not 0 times infinity
