@@ -711,3 +711,46 @@ def test_products_with_scales_far_apart(kind, M):
     s, sx = (s0 * np.float32(2.0 ** 10)), (x0 * np.float32(2.0 ** 120))
     y = f32(int4.gemv_w4a8(x, tensor(sx), packed, tensor(s, BF), z, out_dtype=FL))
     assert not y[:, 0].any()                                 # not 0 times infinity
+
+
+@pytest.mark.parametrize("M,N", [(1, 48), (1, 4200), (4, 48), (16, 8200)])
+def test_products_of_bf16_below_the_normal_range(M, N):
+    """Activations that are whole multiples of bf16's smallest value count."""
+    K, group = 640, 64
+    (codes, _, zeros), w = packed_weight(N, K, group, False, 71)
+    v = rng(72).integers(-3, 4, (M, K)).astype(np.float64)
+    x = tensor(v * 2.0 ** -133, BF)
+    s = torch.full_like(w[1], 1024.0)
+    y = f32(int4.gemv_w4a16(x, w[0], s, w[2], group, FL)).astype(np.float64)
+    want = v @ (codes.astype(np.float64) - ref.per_element(zeros, K, group)).T * 2.0 ** -123
+    assert np.array_equal(y, want)
+
+
+def product_on_gpu(v, w, group):
+    """ref.product in fp64 torch, for large weights."""
+    codes, scales, zeros = w
+    c = codes.reshape(codes.shape[0], -1, 1, 4)
+    c = torch.cat([c & 15, c >> 4], 2).reshape(codes.shape[0], -1).double()
+    K = c.shape[1]
+    spread = lambda t: t.double().repeat_interleave(group, 1)[:, :K]  # noqa: E731
+    s = spread(scales)
+    z = 8.0 if zeros is None else spread(zeros)
+    y = v @ (s * (c - z)).T.contiguous()
+    return y.cpu().numpy(), (v.abs() @ (s * (c + z)).T.contiguous()).cpu().numpy()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("M,N,K,group,symmetric,grouped", [
+    (5, 5000, 8704, 128, False, True), (16, 5000, 8224, 64, True, False), (1, 6000, 9216, 32, False, True),
+    (16, 8200, 8704, 32, True, True), (1, 8300, 12288, 128, False, False), (8, 8250, 12320, 64, False, True),
+    (3, 8200, 8224, 128, True, False), (16, 14336, 4096, 128, False, True)])
+def test_products_in_several_passes(kind, M, N, K, group, symmetric, grouped):
+    """Waves that go over their part of K more than once, with two and four row
+    tiles, K a multiple of 512 and not; and a full batch on a layer's weight."""
+    print(f"[case] passes {kind} M={M} N={N} K={K} group={group} sym={symmetric} grouped={grouped}", flush=True)
+    _, w = packed_weight(N, K, group, symmetric, M + N + K)
+    args, v = activations(kind, M, K, group, grouped, M + K)
+    ystar, a = product_on_gpu(torch.from_numpy(v).to(DEV), w, group)
+    err = np.abs(f32(call(kind, args, w, group, FL)) - ystar)
+    tau = ref.product_bound(a, K)
+    assert np.all(err <= tau), f"{(err > tau).sum()} of {err.size} outputs off; worst {np.max(err / tau)} of the bound"
