@@ -176,3 +176,104 @@ def test_reference_pins():
     assert np.array_equal(v, torch.from_numpy(every[(every & 0x7F) != 0x7F]).view(torch.float8_e4m3fn).double().numpy())
     q, s, h = ref.rmsnorm_quant8([[3.0, -4.0]], None, [[0.0, 0.0]], True, 0.0, 0, False)
     assert list(q[0]) == [95, -127] and abs(s[0, 0] - (4 / np.sqrt(12.5) / 127)) < 1e-9 and list(h[0]) == [3, -4]
+
+
+class _Reached(Exception):
+    """Raised in the place of the look at the device: every check of the binding has passed."""
+
+
+def test_binding_refusals_come_from_its_own_checks(monkeypatch):
+    """Each wrong call is refused for its own reason, before the device is
+    looked at, and right ones get there."""
+    def reached(*tensors):
+        raise _Reached
+    monkeypatch.setattr(int4, "_stream", reached)
+    c, s, z = _weight()
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    x8, xs = torch.zeros((2, 64), dtype=torch.int8), torch.ones((2, 1))
+    w, f8 = torch.zeros((8, 64)), torch.float8_e4m3fn
+    half, wide = torch.zeros((8, 64), dtype=torch.float16), torch.zeros((2, 128), dtype=torch.bfloat16)
+    turned = torch.zeros((64, 2), dtype=torch.bfloat16).t()
+    gapped = torch.zeros((8, 4), dtype=torch.bfloat16)[:, ::2]
+    good = [
+        lambda: int4.quantize(w), lambda: int4.quantize(w.bfloat16(), 32, True),
+        lambda: int4.quantize(w, 32, out=(c, s, z)), lambda: int4.quantize(w, 32, True, out=(c, s, None)),
+        lambda: int4.dequant(c, s, z, 32), lambda: int4.dequant(c, s, None, 32, torch.bfloat16),
+        lambda: int4.dequant(c, s, z, 32, out=w),
+        lambda: int4.gemv_w4a16(x, c, s, z, 32), lambda: int4.gemv_w4a16(x, c, s, None, 32, torch.float32),
+        lambda: int4.gemv_w4a16(x, c, s, z, 32, out=torch.zeros((2, 8))),
+        lambda: int4.gemv_w4a8(x8, xs, c, s, z, 32), lambda: int4.gemv_w4a8(x8.to(f8), torch.ones((2, 2)), c, s, z, 32),
+        lambda: int4.rmsnorm_quant8(x), lambda: int4.rmsnorm_quant8(x, torch.ones(64), x, 0.0, 32, f8),
+        lambda: int4.rmsnorm_quant8(wide[:, :64], residual=wide[:, 64:].float()[:, :64]),
+        lambda: int4.rmsnorm_quant8(x, residual=x, out=(x8, xs, x)),
+    ]
+    for i, f in enumerate(good):
+        with pytest.raises(_Reached):
+            f()
+            pytest.fail(f"right call {i} did not reach the device")
+    packed, flat, side = "a packed weight is", "must be a 2-D tensor", "must be contiguous"
+    bad = [
+        (flat, lambda: int4.quantize(torch.zeros(64))),
+        ("unsupported weight dtype", lambda: int4.quantize(half)),
+        ("group_size=16", lambda: int4.quantize(w, group_size=16)),
+        (side, lambda: int4.quantize(torch.zeros((64, 8)).t())),
+        ("zeros must be None exactly", lambda: int4.quantize(w, 32, True, out=(c, s, z))),
+        ("zeros must be None exactly", lambda: int4.quantize(w, 32, False, out=(c, s, None))),
+        ("out's codes", lambda: int4.quantize(w, 32, out=(c[:, :16], s, z))),
+        ("out's codes", lambda: int4.quantize(w, 32, out=(c.to(torch.int8), s, z))),
+        ("out's scales", lambda: int4.quantize(w, 64, out=(c, s, z))),
+        ("out's scales", lambda: int4.quantize(w, 32, out=(c, gapped, z))),
+        ("out's zeros", lambda: int4.quantize(w, 32, out=(c, s, z[:4]))),
+        (flat, lambda: int4.dequant(c[0], s, z, 32)),
+        (packed, lambda: int4.dequant(c, s, z, 64)),
+        (packed, lambda: int4.dequant(c.to(torch.int8), s, z, 32)),
+        (packed, lambda: int4.dequant(c, s.float(), z, 32)),
+        (packed, lambda: int4.dequant(c, s[:4], z, 32)),
+        (packed, lambda: int4.dequant(c, s, z[:, :1], 32)),
+        (packed, lambda: int4.dequant(c, s, z.to(torch.int8), 32)),
+        (side, lambda: int4.dequant(torch.zeros((32, 8), dtype=torch.uint8).t(), s, z, 32)),
+        (side, lambda: int4.dequant(c, gapped, z, 32)),
+        (side, lambda: int4.dequant(c, s, torch.zeros((2, 8), dtype=torch.uint8).t(), 32)),
+        ("group_size=48", lambda: int4.dequant(c, s, z, 48)),
+        ("unsupported output dtype", lambda: int4.dequant(c, s, z, 32, out_dtype=torch.float16)),
+        ("unsupported output dtype", lambda: int4.dequant(c, s, z, 32, out=half)),
+        ("out must be a contiguous", lambda: int4.dequant(c, s, z, 32, out=torch.zeros((8, 32)))),
+        ("out must be a contiguous", lambda: int4.dequant(c, s, z, 32, out=torch.zeros((64, 8)).t())),
+        ("2-D bfloat16", lambda: int4.gemv_w4a16(x.float(), c, s, z, 32)),
+        ("x has 32 columns", lambda: int4.gemv_w4a16(x[:, :32], c, s, z, 32)),
+        (flat, lambda: int4.gemv_w4a16(x[0], c, s, z, 32)),
+        (side, lambda: int4.gemv_w4a16(turned, c, s, z, 32)),
+        (packed, lambda: int4.gemv_w4a16(x, c, s, z, 128)),
+        ("unsupported output dtype", lambda: int4.gemv_w4a16(x, c, s, z, 32, torch.float16)),
+        ("out must be a contiguous", lambda: int4.gemv_w4a16(x, c, s, z, 32, out=torch.zeros((2, 9)))),
+        ("out must be a contiguous", lambda: int4.gemv_w4a16(x, c, s, z, 32, out=torch.zeros((8, 2)).t())),
+        ("unsupported activation dtype", lambda: int4.gemv_w4a8(x, xs, c, s, z, 32)),
+        ("x_scales must be", lambda: int4.gemv_w4a8(x8, xs.double(), c, s, z, 32)),
+        ("x_scales must be", lambda: int4.gemv_w4a8(x8, torch.ones((2, 3)), c, s, z, 32)),
+        ("x_scales must be", lambda: int4.gemv_w4a8(x8, torch.ones(2), c, s, z, 32)),
+        (side, lambda: int4.gemv_w4a8(x8, torch.ones((2, 4))[:, ::2], c, s, z, 32)),
+        (flat, lambda: int4.rmsnorm_quant8(x[0])),
+        ("unsupported x dtype", lambda: int4.rmsnorm_quant8(half)),
+        ("unsupported output dtype", lambda: int4.rmsnorm_quant8(x, out_dtype=torch.uint8)),
+        ("eps=-1.0", lambda: int4.rmsnorm_quant8(x, eps=-1.0)),
+        ("eps=nan", lambda: int4.rmsnorm_quant8(x, eps=float("nan"))),
+        ("eps=inf", lambda: int4.rmsnorm_quant8(x, eps=float("inf"))),
+        ("group_size=48", lambda: int4.rmsnorm_quant8(x, group_size=48)),
+        ("weight must be", lambda: int4.rmsnorm_quant8(x, torch.ones(32))),
+        ("weight must be", lambda: int4.rmsnorm_quant8(x, torch.ones(128)[::2])),
+        ("unsupported weight dtype", lambda: int4.rmsnorm_quant8(x, torch.ones(64, dtype=torch.float16))),
+        ("residual must have", lambda: int4.rmsnorm_quant8(x, residual=torch.zeros((1, 64)))),
+        ("residual must have", lambda: int4.rmsnorm_quant8(x.float(), residual=x)),
+        ("x's rows must be contiguous", lambda: int4.rmsnorm_quant8(turned)),
+        ("residual's rows must be contiguous", lambda: int4.rmsnorm_quant8(x, residual=turned)),
+        ("sum must be None exactly", lambda: int4.rmsnorm_quant8(x, out=(x8, xs, x))),
+        ("sum must be None exactly", lambda: int4.rmsnorm_quant8(x, residual=x, out=(x8, xs, None))),
+        ("out's sum", lambda: int4.rmsnorm_quant8(x, residual=x, out=(x8, xs, x.float()))),
+        ("out's sum", lambda: int4.rmsnorm_quant8(x, residual=x, out=(x8, xs, turned))),
+        ("out's scales", lambda: int4.rmsnorm_quant8(x, group_size=32, out=(x8, xs, None))),
+        ("out's codes", lambda: int4.rmsnorm_quant8(x, out=(x8[:, :32], xs, None))),
+    ]
+    for i, (why, f) in enumerate(bad):
+        with pytest.raises(ValueError, match=why):
+            f()
+            pytest.fail(f"call {i} was accepted")
