@@ -754,3 +754,29 @@ def test_products_in_several_passes(kind, M, N, K, group, symmetric, grouped):
     err = np.abs(f32(call(kind, args, w, group, FL)) - ystar)
     tau = ref.product_bound(a, K)
     assert np.all(err <= tau), f"{(err > tau).sum()} of {err.size} outputs off; worst {np.max(err / tau)} of the bound"
+
+
+def test_every_entry_point_refuses_a_capturing_stream():
+    """Nothing is launched and no output changes."""
+    _, (c, s, z) = packed_weight(8, 64, 32, False, 1)
+    x, x8 = torch.ones((1, 64), dtype=BF, device=DEV), torch.ones((1, 64), dtype=torch.int8, device=DEV)
+    xs, w = torch.ones((1, 1), device=DEV), torch.ones((8, 64), device=DEV)
+    y, d = torch.full((1, 8), 7.0, device=DEV), torch.full((8, 64), 7.0, device=DEV)
+    q, qs, h = torch.full_like(x8, 7), torch.full_like(xs, 7.0), torch.full_like(x, 7.0)
+    c2, s2, z2 = torch.full_like(c, 7), torch.full_like(s, 7.0), torch.full_like(z, 7)
+    marker = torch.zeros(1, device=DEV)
+    torch.cuda.synchronize()
+    L, side, graph = int4.lib(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = ctypes.c_void_p(side.cuda_stream)
+    with torch.cuda.graph(graph, stream=side):
+        marker.add_(1.0)                             # one node, so the graph is not empty; it is never replayed
+        got = [L.int4_quantize(p(w), int4.F32, 8, 64, 32, p(c2), p(s2), p(z2), st),
+               L.int4_dequant(p(c), p(s), p(z), 8, 64, 32, p(d), int4.F32, st),
+               L.int4_gemv_w4a16(p(x), p(c), p(s), p(z), 32, 1, 8, 64, p(y), int4.F32, st),
+               L.int4_gemv_w4a8(p(x8), int4.I8, p(xs), 0, p(c), p(s), p(z), 32, 1, 8, 64, p(y), int4.F32, st),
+               L.int4_rmsnorm_quant8(p(x), int4.BF16, 64, p(x), int4.BF16, 64, None, 0, 1e-6, 1, 64, 0, int4.I8, p(q),
+                                     p(qs), p(h), st)]
+    torch.cuda.synchronize()
+    assert got == [nv.ERR_CAPTURE] * 5
+    assert all(bool((t.float() == 7).all()) for t in (y, d, q, qs, h, c2, s2, z2))
