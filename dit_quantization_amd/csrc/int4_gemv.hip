@@ -219,12 +219,13 @@ __global__ __launch_bounds__(256) void int4_gemv_m1_kernel(Int4Act x, Int4Weight
 // and 1.2e-6 for INT8 instead of 3.4e-8 and 2.5e-8).
 //
 // Bound: memory and, right behind it, vector issue.  14336 x 4096, bf16, M = 1:
-// 30.8 MB in 8.2 us a call (3.8 TB/s; the DMA alone, with nothing computed,
-// takes 6.5-6.9); about 850 vector instructions a wave are 2.8 us of issue, half
-// of them unpacking codes.  INT8 unpacks in 3 instructions for 8 codes instead
-// of 7 and takes 7.4 us; M = 16: INT8 8.7, E4M3 with grouped scales 9.4, bf16
-// 9.7 us.  4096 x 14336, bf16: M = 1 9.1, M = 5 10.6, M = 16 13.3 us; a workgroup
-// takes 8 us even where only a quarter of the CUs have one, reading x among it.
+// 30.8 MB in 8.4 us a call from memory (3.7 TB/s; 8.0 from the last-level cache,
+// where the DMA alone, with nothing computed, takes 6.5-6.9); about 910 vector
+// instructions a wave are 3.0 us of issue, half of them unpacking codes.  INT8
+// unpacks in 3 instructions for 8 codes instead of 7 and takes 7.7 us; M = 16:
+// INT8 9.1, E4M3 with grouped scales 9.9, bf16 10.1 us.  4096 x 14336, bf16: M = 1
+// 10.8, M = 16 13.9 us (9.4 and 13.3 from the cache); a workgroup takes 7 us even
+// where only a quarter of the CUs have one, reading x among it.
 //
 // E4M3 activations are widened to bf16 as well: the FP8 matrix instruction
 // keeps too few bits of its sums (9e-5 off, relative, after 160 products,
@@ -600,15 +601,28 @@ __global__ __launch_bounds__(NW * 64) void int4_gemv_mfma_kernel(Int4Act x, Int4
   }
 }
 
-// Waves and rows per workgroup, from a sweep over N = 256..28672, K =
-// 512..14336 and M = 1..16 of the three types (us a call, back to back):
+// Waves and rows per workgroup, from a sweep over 16 and 32 and 64 rows at the
+// sizes named here, M = 1 and 16, all types, groups of 128 (us a call, queued
+// back to back, the weights from memory):
 //  * N <= 4096: 16 rows, so that up to 256 CUs have a workgroup each; 16 waves
 //    where K has more than one pass for each of 8 (4096 x 14336, bf16, M =
-//    16: 13.2 with 16, 14.7 with 8; 4096 x 4096: 6.0 with either);
-//  * N <= 8192: 32 rows for the same reason (8192 x 4096, INT8, M = 16: 6.5;
-//    16 rows 6.8, 64 rows 7.7);
+//    16: 14.2 with 16, 14.9 with 8; M = 1: 9.5, 10.1; 4096 x 4096: 6.4, 6.3);
+//    just above that length 8 waves are still as good (4096 x 8192, M = 1: 7.7
+//    with 16, 7.2 with 8);
+//  * N <= 8192: 32 rows for the same reason (8192 x 4096, INT8, M = 16: 6.8;
+//    16 rows 7.2, 64 rows 7.8; 5120 x 5120, bf16, M = 16: 8.4, 10.7, 11.7);
 //  * above: 64 rows, x being read once per workgroup (14336 x 4096, INT8, M =
-//    16: 8.7; 32 rows 10.7, 16 rows 11.7).
+//    16: 9.1; 32 rows 11.3, 16 rows 12.3; 28672 x 4096, bf16, M = 1: 15.1, 17.6,
+//    16.6).
+// A workgroup of 64 rows fills a CU's LDS, so N a little above 16384 takes a
+// second, nearly empty round: there 16 rows are faster at M = 1 (17408 x 5120,
+// bf16: 15.6 instead of 19.7; 18944 x 3584: 11.6, 13.4) and no shape gains at M
+// = 16 (22.1 against 21.5 and 22.2; 15.9 and 16.0).
+//
+// x of 5 to 8 rows is read as 8 rows, not 16: 14336 x 4096, M = 5, bf16 8.6 us
+// instead of 9.1, INT8 8.0, 8.2; 4096 x 14336, M = 8, bf16 10.8, 12.0; 28672 x
+// 8192, M = 5, bf16 31.2, 32.6 (the weights of the first two from the last-level
+// cache).
 template <Act A, bool GX>
 hipError_t launch_mfma(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, int G, void* y, int b,
                        hipStream_t stream) {
@@ -639,10 +653,11 @@ hipError_t launch_mfma(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t
   return hipGetLastError();
 }
 
-// One row of few weights goes to the dot products, which start sooner (1024 x
-// 14336, bf16: 4.8 us, the matrix kernel 7.7; 4096 x 8192: 6.4, 6.8); a large
-// weight to the matrix kernel, which reads longer runs (4096 x 14336: 11.4, 9.1;
-// 14336 x 4096: 9.0, 8.2; 8192 x 8192: 9.9, 9.3).  K is split over 2 or 4 waves.
+// One row of few weights goes to the dot products, which start sooner (bf16, us
+// a call with the weights from memory: 1024 x 4096 3.4, the matrix kernel 4.2;
+// 1024 x 14336 5.9, 7.8; 4096 x 4096 4.8, 5.0; 4096 x 8192 6.6, 7.1); a large weight
+// to the matrix kernel, which reads longer runs (4096 x 14336: 11.7, 10.5; 14336
+// x 4096: 9.2, 8.4; 8192 x 4096: 6.3, 6.0).  K is split over 2 or 4 waves.
 template <Act A>
 hipError_t launch_gemv(const Int4Act& x, const Int4Weight& w, int64_t M, int64_t N, int64_t K, void* y, int b,
                        hipStream_t stream) {

@@ -17,9 +17,9 @@
 // range (or 0, as it is where all products underflow) it is taken again in fp64.
 //
 // Bound by memory at long rows (4096 x 4096, bf16 with a bf16 residual, E4M3 in
-// groups of 128: 118 MB in 23.5 us, 5.0 TB/s; a large copy runs at 5.1), with
+// groups of 128: 118 MB in 23.7 us, 5.0 TB/s; a large copy runs at 5.1), with
 // vector issue behind it (34 instructions an element there are 15 us, 22 with
-// one INT8 scale a row); 110593 x 128 to INT8: 43 MB in 9.9 us.
+// one INT8 scale a row); 110593 x 128 to INT8: 43 MB in 10.0 us, 11.6 from memory.
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T, T >= 512 ? (V <= 2 ? 8 : 4) : 1)
   // nor more than code 0.
   const auto in_range = [](float top) { return top >= 0x1p-100f && top <= 0x1p126f; };
   // Maximum |h w| of vector v in fp64, of h and the weight as they lie in
-  // memory: kept in registers for this rare path, they would cost two waves a
+  // memory: kept in registers for this rare path, they would cost a wave a
   // SIMD.
   const auto wide_top_of = [&](int v) {
     const int i = fresh(t + T * v);

@@ -23,6 +23,19 @@
  * (INT4_E4M3), with fp32 scales [rows, 1], or [rows, ceil(cols / group)] for
  * groups of `group` columns; the value is scale * code.
  *
+ * The format is the grouping and arithmetic of such checkpoints, not their
+ * files: codes, scales and zero points have this library's own order and types
+ * (GPTQ and AWQ files pack int32 words in orders of their own and scale in
+ * fp16, three bits more than bf16).  Nothing here reads them; int4_quantize
+ * makes a weight from its 16- or 32-bit values.
+ *
+ * The products take up to 16 rows.  For more, int4_dequant makes a bf16 weight
+ * for a library product, and 8-bit activations are scale * code in any tensor
+ * library, or the norm is taken in 16 bits.
+ *
+ * These entry points came to the library at version 1.8.1 without a change of
+ * nvfp4_version(), which counts nvfp4.h's interface: look them up by symbol.
+ *
  * Statuses and conventions are nvfp4.h's: device pointers of the current
  * device, calls asynchronous on `stream`, nothing allocated, every argument
  * checked before a launch, NVFP4_ERR_CAPTURE on a stream that is being
@@ -87,7 +100,8 @@ int int4_dequant(const uint8_t* codes, const void* scales, const uint8_t* zeros,
  *   sum is the difference of sum x code and z sum x, then scaled and added: the
  *   fp32 result is off by at most
  *     2^-24 (129 sum_k |x| s (code + z) + (K / 32 + 26) sum_r |t_r|)
- *   with t_r the terms of the sum over runs of 32 elements.
+ *   with t_r the terms of the sum over runs of 32 elements (short of sums
+ *   outside fp32's normal range).
  */
 int int4_gemv_w4a16(const void* x, const uint8_t* codes, const void* scales, const uint8_t* zeros, int group,
                     int64_t M, int64_t N, int64_t K, void* y, int y_dtype, void* stream);
