@@ -1,0 +1,140 @@
+// Weights to E4M3 with a scale for each 128 x 128 block, and activations (or
+// SiLU(gate) x) to INT8 or E4M3 with a scale for each group of 32, 64 or 128
+// columns (definitions: include/fp8.h).
+//
+// Both are one pass over memory: the values that share a scale stay in
+// registers between the maximum and the codes.  Codes are decided by fp64
+// quotients (the multiply-add runs at the fp32 rate here).
+#include "device_common.hpp"
+#include "encode8.hpp"
+#include "fp8_kernels.hpp"
+#include "lanes.hpp"
+
+namespace nvfp4 {
+
+// ---- weights.  A workgroup of 256 threads has one block: 16 lanes a row of
+// 128 columns (8 each), 16 rows at a time, 8 vectors a thread.
+template <bool BF>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(const void* __restrict__ x, int64_t stride, int64_t rows,
+                                                           int cols, int blocks_k, uint8_t* __restrict__ codes,
+                                                           float* __restrict__ scales) {
+  constexpr int V = 8;
+  const int bk = (int)(blockIdx.x % (unsigned)blocks_k);
+  const int64_t bn = blockIdx.x / (unsigned)blocks_k;
+  const int lane = threadIdx.x & 15, row0 = threadIdx.x >> 4;
+  const int col = 128 * bk + 8 * lane;
+  Vec8<BF> v[V];
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t r = 128 * bn + row0 + 16 * i;
+    v[i].zero();
+    if (r < rows && col < cols) v[i].load(x, r * stride + col);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i].at(j)));
+  const auto most = [](float a, float b) { return fmaxf(a, b); };
+  top = lanes_all<64>(top, most);
+  __shared__ float part[4];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  const float s = scale_for((double)top, 448.0);
+  if (threadIdx.x == 0) scales[blockIdx.x] = s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int64_t r = 128 * bn + row0 + 16 * i;
+    if (r < rows && col < cols) {
+      double d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = (double)v[i].at(j);
+      *reinterpret_cast<u32x2*>(codes + r * cols + col) = encode_quotients(d, s, true);
+    }
+  }
+}
+
+hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t rows, int64_t cols, uint8_t* codes,
+                               float* scales, hipStream_t stream) {
+  const int blocks_k = (int)((cols + 127) / 128);
+  // at most 2^22 workgroups a launch (a launch counts its threads in 32 bits), whole rows of blocks
+  const int64_t step = 128 * (((int64_t)1 << 22) / blocks_k);
+  for (int64_t r0 = 0; r0 < rows; r0 += step) {
+    const int64_t n = rows - r0 < step ? rows - r0 : step;
+    const void* xr = reinterpret_cast<const char*>(x) + r0 * stride * (bf16 ? 2 : 4);
+    uint8_t* cr = codes + r0 * cols;
+    float* sr = scales + r0 / 128 * blocks_k;
+    const dim3 grid((unsigned)((n + 127) / 128 * blocks_k));
+    if (bf16)
+      hipLaunchKernelGGL(fp8_quantize_kernel<true>, grid, dim3(256), 0, stream, xr, stride, n, (int)cols, blocks_k, cr, sr);
+    else
+      hipLaunchKernelGGL(fp8_quantize_kernel<false>, grid, dim3(256), 0, stream, xr, stride, n, (int)cols, blocks_k, cr, sr);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// ---- activations.  A row is cut into slots of 8 columns, filled up to whole
+// groups, and slots go to threads in order, so that a group is 4, 8 or 16
+// neighbouring lanes.
+template <bool BF, bool SILU>
+__global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, double q) {
+  const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = (int64_t)(at / slots);
+  const int i = (int)(at % slots), c = 8 * i;
+  const bool live = r < a.rows && c < a.cols;
+  Vec8<BF> x, g;
+  x.zero();
+  g.zero();
+  if (live) {
+    x.load(a.x, r * a.x_stride + c);
+    if (SILU) g.load(a.gate, r * a.gate_stride + c);
+  }
+  double y[8], top = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = (double)x.at(j);
+    if (SILU) {
+      const double v = (double)g.at(j);
+      y[j] *= v / (1.0 + exp(-v));
+    }
+    top = fmax(top, fabs(y[j]));
+  }
+  const int L = a.group / 8;
+  top = lanes_all(top, L, [](double p, double t) { return p > t ? p : t; });
+  const float s = scale_for(top, q);
+  if (live) {
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint8_t*>(a.codes) + r * a.cols + c) = encode_quotients(y, s, a.e4m3);
+    if ((i & (L - 1)) == 0) a.scales[r * (int64_t)(slots / L) + i / L] = s;
+  }
+}
+
+hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
+  const int L = all.group / 8;
+  const uint32_t slots = (uint32_t)((all.cols + all.group - 1) / all.group * L);
+  // at most 2^31 threads a launch, whole rows
+  const int64_t step = ((int64_t)1 << 31) / slots;
+  for (int64_t r0 = 0; r0 < all.rows; r0 += step) {
+    ActArgs a = all;
+    const int size = a.bf16 ? 2 : 4;
+    a.rows = all.rows - r0 < step ? all.rows - r0 : step;
+    a.x = reinterpret_cast<const char*>(all.x) + r0 * all.x_stride * size;
+    if (a.gate) a.gate = reinterpret_cast<const char*>(all.gate) + r0 * all.gate_stride * size;
+    a.codes = reinterpret_cast<char*>(all.codes) + r0 * all.cols;
+    a.scales = all.scales + r0 * (slots / L);
+    const dim3 grid((unsigned)((a.rows * slots + 255) / 256));
+    const double q = a.e4m3 ? 448.0 : 127.0;
+#define ACT_CASE(BF, SILU) \
+  hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU>), grid, dim3(256), 0, stream, a, slots, q)
+    if (a.gate && a.bf16) ACT_CASE(true, true);
+    else if (a.gate) ACT_CASE(false, true);
+    else if (a.bf16) ACT_CASE(true, false);
+    else ACT_CASE(false, false);
+#undef ACT_CASE
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace nvfp4
