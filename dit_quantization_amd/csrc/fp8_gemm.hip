@@ -1,6 +1,8 @@
 // Block-scaled FP8 product y = x^ W^^T (definition: include/fp8.h):
 //   y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{k in b} x[m, k] w[n, k]
 // with b the blocks of 128 columns.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "fp8_kernels.hpp"
 #include "lanes.hpp"
@@ -18,12 +20,14 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
 }
 
+// NaN, infinity, subnormal or zero.
+__device__ __forceinline__ bool not_normal(float v) { return __builtin_amdgcn_classf(v, 0x2F7); }
+
 // acc += xs ws d.  The product of the scales is used where it is a normal number
 // in all lanes; elsewhere it could leave fp32's range although xs ws d does not.
 __device__ __forceinline__ void add_scaled(f32x4 d, float ws, float xs, f32x4& acc) {
-  constexpr int kNotNormal = 0x003 | 0x004 | 0x200 | 0x010 | 0x080 | 0x020 | 0x040;  // NaN, infinity, subnormal, zero
   const float s = ws * xs;
-  if (__ballot(__builtin_amdgcn_classf(s, kNotNormal)) == 0) {
+  if (__ballot(not_normal(s)) == 0) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d[r], s, acc[r]);
   } else {
@@ -151,6 +155,342 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
     }
 }
 
+// ---- many rows.  A workgroup of WM x WN waves has BM rows of x and BN rows of
+// the weight, a wave TM x TN tiles of 16 x 16.  One step a block of 128
+// columns: both operands' rows go from memory to LDS directly (two stages, one
+// filled while the other is read), 16-byte chunks XOR-swizzled so that the
+// fragment reads of 16 rows meet all banks.  The weight is the instruction's
+// first operand, so a lane's results are 4 rows of the weight for one row of
+// x, and one factor xs ws serves them all: a block's sums start from zero in
+// the matrix instruction and are added to the running ones by a multiply-add,
+// which the vector units do while the matrix unit has the next tiles.
+// WIDE: widened to bf16 on the way to the matrix instruction (fp32 outputs).
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Consecutive workgroups go to different XCDs (round robin over 8): the tile
+// for workgroup `bid`, so that each XCD has a contiguous run of tiles.
+__device__ __forceinline__ int xcd_run(int bid, int n) {
+  const int q = n >> 3, r = n & 7, xcd = bid & 7;
+  return xcd * q + min(xcd, r) + (bid >> 3);
+}
+
+template <int BM, int BN, int WM, int WN, bool WIDE>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2))) void fp8_gemm_tile_kernel(Fp8Product p) {
+  constexpr int NT = WM * WN * 64, NW = WM * WN;
+  constexpr int WBM = BM / WM, WBN = BN / WN;        // a wave's tile
+  constexpr int TM = WBM / 16, TN = WBN / 16;
+  constexpr int XD = BM * 8 / NT, WD = BN * 8 / NT;  // 16-byte loads a lane and step
+  constexpr int XSW = (BM + 63) / 64;                // waves that load x's scales
+  constexpr int LAST = 2, WB = 4;                    // rows of tiles behind a step's second barrier; fragments held
+  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && WD % 2 == 0 && XSW < NW && TN % 4 == 0, "tile and waves");
+  static_assert(128 % WBN == 0, "a wave's rows of the weight share a scale");
+  struct Stages {
+    u32x4 x[2][BM * 8], w[2][BN * 8];
+    f32x4 scales[2][NW * 64], unused[NW * 64];  // of 4 blocks a row
+  };
+  __shared__ __attribute__((aligned(16))) Stages st;
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (int)((p.M + BM - 1) / BM);
+  // tiles in groups of 4 tiles of x, so that an XCD's tiles share rows of both operands in its L2
+  constexpr int GROUP = 4;
+  const int bid = xcd_run((int)blockIdx.x, tiles_m * tiles_n);
+  const int first = bid / (GROUP * tiles_n) * GROUP, gsize = min(tiles_m - first, GROUP);
+  const int in = bid % (GROUP * tiles_n);
+  const int64_t m0 = (int64_t)(first + in % gsize) * BM;
+  const int n0 = in / gsize * BN;
+  const int rows = (int)min((int64_t)BM, p.M - m0), wrows = min(BN, p.N - n0);
+  const int G = (p.K + 127) / 128;
+
+  // Loads of 8 rows: lane l has row l / 8 and stores to slot l % 8 its chunk
+  // (l % 8) ^ (row / 2 % 8); the 8 rows start at a multiple of 8.  A wave's
+  // loads of the weight are half of the first halves of the WN waves' rows,
+  // half of the second halves.
+  const __amdgpu_buffer_rsrc_t xbuf = make_buf(p.x + m0 * p.K, (uint32_t)rows * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t wbuf = make_buf(p.w + (int64_t)n0 * p.K, (uint32_t)wrows * (uint32_t)p.K);
+  const auto w_at = [&](int j) {
+    const int t = 8 * (wave * (WD / 2) + j % (WD / 2)), half = j / (WD / 2);
+    return t / (WBN / 2) * WBN + half * (WBN / 2) + t % (WBN / 2);
+  };
+  // (x's rows go by the same order where there are as many: fewer offsets)
+  const auto x_at = [&](int j) { return XD == WD ? w_at(j) : 8 * (wave * XD + j); };
+  const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));
+  const auto chunk_at = [&](int row) { return chunk ^ (uint32_t)((row & 8) << 3); };
+  uint32_t x_off[XD], w_off[WD];
+#pragma unroll
+  for (int j = 0; j < XD; ++j) x_off[j] = (uint32_t)(x_at(j) + (lane >> 3)) * (uint32_t)p.K + chunk_at(x_at(j));
+#pragma unroll
+  for (int j = 0; j < WD; ++j) w_off[j] = (uint32_t)(w_at(j) + (lane >> 3)) * (uint32_t)p.K + chunk_at(w_at(j));
+  // The first waves load x's scales (a row past the end takes the last one's: a
+  // normal number), the next one those of the weight.
+  const __amdgpu_buffer_rsrc_t sbuf = make_buf(p.xs + m0 * G, (uint32_t)rows * (uint32_t)G * 4u);
+  const __amdgpu_buffer_rsrc_t wsbuf =
+      make_buf(p.ws + (int64_t)(n0 / 128) * G, (uint32_t)((wrows + 127) / 128) * (uint32_t)G * 4u);
+  const __amdgpu_buffer_rsrc_t scbuf = wave < XSW ? sbuf : wsbuf;
+  const uint32_t sc_off = (uint32_t)(wave < XSW ? min(tid, rows - 1) : lane) * (uint32_t)G * 4u;
+  // Load q of block b (the last one again past the end): 0 .. XD - 1 x, then
+  // the first and the second half of the weight's.
+  constexpr int L1 = XD + WD / 2, L2 = WD / 2;
+  const auto dma = [&](int stage, int blk, int q) {
+    const int b = min(blk, G - 1);
+    const uint32_t k = 128u * (uint32_t)b;
+    if (q < XD) {
+      // chunks past a row's end: zeros for x, and whatever the next row of the
+      // weight holds (zeros behind the last) for the weight
+      buffer_to_lds16(xbuf, st.x[stage] + 8 * x_at(q), k + chunk_at(x_at(q)) < (uint32_t)p.K ? x_off[q] : kBufOOB, k);
+    } else {
+      buffer_to_lds16(wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
+    }
+  };
+  // The scales of the 4 blocks from b on, a row 16 bytes (past a row's end
+  // whatever the next one holds), every fourth time; in between the load
+  // fetches nothing and goes nowhere.
+  const auto dma_scales = [&](int b) {
+    const bool due = (b & 3) == 0 && b < G;
+    buffer_to_lds16(scbuf, reinterpret_cast<u32x4*>((due ? st.scales[(b >> 2) & 1] : st.unused) + 64 * wave),
+                    due ? sc_off : kBufOOB, 4u * (uint32_t)min(b, G - 1));
+  };
+
+  // Fragments: chunks g and g + 4 of a row, the same columns of both operands.
+  const int sw = (l16 >> 1) & 7;
+  const int x_row = (wm * WBM + l16) * 8, w_row = (wn * WBN + l16) * 8;
+  const int x0 = x_row + (g ^ sw), x1 = x_row + ((g + 4) ^ sw), w0 = w_row + (g ^ sw), w1 = w_row + ((g + 4) ^ sw);
+  u32x4 xf[TM][2], wf[WB][2];
+  float s[TM], xsc[TM], wsc, s_last = 0.0f;
+  bool odd = false;
+  const auto load_x = [&](int stage, int j, int h) { xf[j][h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
+  const auto load_w = [&](int stage, int i, int h) { wf[i % WB][h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
+  const auto load_scales = [&](int b) {
+    const float* of = reinterpret_cast<const float*>(st.scales[(b >> 2) & 1]) + (b & 3);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) xsc[j] = of[4 * (wm * WBM + 16 * j + l16)];
+    wsc = of[4 * (64 * XSW + wn * WBN / 128)];
+  };
+  // factors of a block; those that are no normal number count as 0 here
+  const auto factors = [&] {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const float v = xsc[j] * wsc;
+      const bool o = not_normal(v);
+      s[j] = o ? 0.0f : v;
+      odd |= o;
+    }
+  };
+
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  const auto multiply = [&](int i, int j) {
+    const u32x4 *a = wf[i % WB], *b = xf[j];
+    f32x4 d = {0, 0, 0, 0};
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(a[h / 2][2 * (h & 1)], a[h / 2][2 * (h & 1) + 1]),
+                                                    widen8(b[h / 2][2 * (h & 1)], b[h / 2][2 * (h & 1) + 1]), d, 0, 0, 0);
+    } else {
+      const i32x8 av = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
+      const i32x8 bv = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
+      d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, d, 0, 0, 0, 0, 0, 0);
+    }
+    return d;
+  };
+  // Tile q of a step: rows 0 .. TN - LAST - 1, then the columns of the last
+  // rows.  A tile's sums are added two tiles later, while the matrix unit has
+  // the next ones (the first two of a step add the last two of the step before).
+  constexpr int TILES = TN * TM, T0 = (TN - LAST) * TM, LAG = 2;
+  f32x4 d[4] = {};
+  const auto tile_i = [](int q) { return q < T0 ? q / TM : TN - LAST + (q - T0) % LAST; };
+  const auto tile_j = [](int q) { return q < T0 ? q % TM : (q - T0) / LAST; };
+  const auto add = [&](int q, float f) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[tile_i(q)][tile_j(q)][r] = __builtin_fmaf(d[q % 4][r], f, acc[tile_i(q)][tile_j(q)][r]);
+  };
+  static_assert(TILES % 4 == 0 && LAG <= LAST, "d's entries follow the tiles; the last two tiles share a factor");
+  const auto tile = [&](int q) {
+    d[q % 4] = multiply(tile_i(q), tile_j(q));
+    if (q >= LAG) add(q - LAG, s[tile_j(q - LAG)]);
+    else add(TILES + q - LAG, s_last);
+  };
+  // All waves are past their reads of what the next loads overwrite, and all
+  // loads but the newest `n` a wave have landed.
+  const auto meet = [&](auto n) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(decltype(n)::value));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // A step meets twice: in front of row A, from which on the second half of
+  // the weight's rows is read, all waves have block b's x and first half in
+  // registers, so block b + 2's go into their place; in front of the last
+  // rows the same for the second half, and block b + 1's x and first half are
+  // there.  Every load has one and a half steps to land.
+  constexpr int A = TN / 2 - 2;
+  constexpr int SLACK = L1 + 1 + L2;  // loads of a block, one for scales among them
+  const auto step = [&](int b, int cur) {
+    const int nxt = cur ^ 1;
+#pragma unroll
+    for (int q = 0; q < T0; ++q) {
+      const int i = q / TM, c = q % TM;
+      if (q == A * TM) meet(std::integral_constant<int, SLACK>{});
+      if (c < 2) load_w(cur, i + 2, c);
+      if (q >= A * TM && q - A * TM < L1) dma(cur, b + 2, q - A * TM);
+      if (q == T0 - 1) dma_scales(b + 2);
+      tile(q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    static_assert(T0 - A * TM >= L1 || TM == 2, "");
+#pragma unroll
+    for (int q = T0 - A * TM; q < L1; ++q) dma(cur, b + 2, q);
+    meet(std::integral_constant<int, SLACK>{});
+    load_scales(b + 1);
+#pragma unroll
+    for (int q = T0; q < TILES; ++q) {
+      const int c = (q - T0) / LAST, in_c = (q - T0) % LAST;
+      if (q - T0 < L2) dma(cur, b + 2, L1 + q - T0);
+      tile(q);
+      if (q - T0 < 4) load_w(nxt, (q - T0) / 2, (q - T0) % 2);
+      if (in_c == LAST - 1) {
+        load_x(nxt, c, 0);
+        load_x(nxt, c, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int q = TILES - T0; q < L2; ++q) dma(cur, b + 2, L1 + q);
+    s_last = s[TM - 1];
+    factors();
+  };
+  static_assert(TM >= 2, "a tile a fragment's load");
+
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+#pragma unroll
+    for (int q = 0; q < L1; ++q) dma(b, b, q);
+    dma_scales(b);
+#pragma unroll
+    for (int q = L1; q < L1 + L2; ++q) dma(b, b, q);
+  }
+  meet(std::integral_constant<int, SLACK + L2>{});
+  load_scales(0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) load_x(0, j, h);
+    load_w(0, 0, h);
+    load_w(0, 1, h);
+  }
+  factors();
+  int b = 0;
+  for (; b + 2 <= G; b += 2) {
+    step(b, 0);
+    step(b + 1, 1);
+  }
+  if (b < G) step(b, 0);
+#pragma unroll
+  for (int q = TILES - LAG; q < TILES; ++q) add(q, s_last);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
+
+  // Products of scales that are no normal number could leave fp32's range
+  // although xs ws d does not: they counted as 0 above, and their blocks are
+  // taken again, straight from memory.
+  if (__ballot(odd)) {
+#pragma unroll 1
+    for (b = 0; b < G; ++b) {
+      const float wsc = p.ws[(int64_t)(min(n0 + wn * WBN, p.N - 1) / 128) * G + b];
+      double f[TM];
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const float v = p.xs[(m0 + min(wm * WBM + 16 * j + l16, rows - 1)) * G + b];
+        const bool o = not_normal(v * wsc);
+        f[j] = o ? (double)v * (double)wsc : 0.0;
+        any |= o;
+      }
+      if (!__ballot(any)) continue;
+      const auto fragment = [&](__amdgpu_buffer_rsrc_t buf, int r, u32x4 (&q)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k = 128u * (uint32_t)b + 64u * h + 16u * (uint32_t)g;
+          q[h] = __builtin_amdgcn_raw_buffer_load_b128(buf, k < (uint32_t)p.K ? (uint32_t)r * (uint32_t)p.K + k : kBufOOB, 0, 0);
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < TM; ++j) fragment(xbuf, wm * WBM + 16 * j + l16, xf[j]);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        fragment(wbuf, wn * WBN + 16 * i + l16, wf[i % WB]);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const f32x4 e = multiply(i, j);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += (float)((double)e[r] * f[j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // A lane has, of a tile, one row of x and four rows of the weight.  bf16
+  // rows go through LDS (a wave's own part of the stages, 16-byte chunks
+  // swizzled by the row) and out as 16 bytes a lane, non-temporal: y is not
+  // read again here.
+  constexpr int RC = WBN / 8;  // 16-byte chunks of a wave's bf16 rows
+  const int nw = n0 + wn * WBN;
+  if (!WIDE && (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
+    static_assert(WBM * WBN * 2 * NW <= (int)sizeof(st) && WBM * RC % 64 == 0, "the tile fits the stages");
+    __builtin_amdgcn_s_barrier();  // every wave has read the stages (its reads are waited for above)
+    uint32_t* out = reinterpret_cast<uint32_t*>(&st) + wave * (WBM * WBN / 2);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int m = 16 * j + l16;
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const f32x4 v = acc[i][j];
+        *reinterpret_cast<u32x2*>(out + (m * RC + ((2 * i + (g >> 1)) ^ (l16 & (RC - 1)))) * 4 + 2 * (g & 1)) =
+            u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    __builtin_amdgcn_wave_barrier();
+    uint16_t* y = reinterpret_cast<uint16_t*>(p.y);
+#pragma unroll
+    for (int q = 0; q < WBM * RC / 64; ++q) {
+      const int m = (64 * q + lane) / RC, c = lane & (RC - 1);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(out + (m * RC + (c ^ (m & 15 & (RC - 1)))) * 4);
+      const int row = wm * WBM + m, n = nw + 8 * c;
+      if (row < rows && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (m0 + row) * p.N + n));
+    }
+    return;
+  }
+  const bool fours = !p.bf16 && (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int m = wm * WBM + 16 * j + l16;
+    if (m >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int n = nw + 16 * i + 4 * g;
+      const int64_t at = (m0 + m) * p.N + n;
+      if (fours) {
+        if (n < p.N) __builtin_nontemporal_store(acc[i][j], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at));
+        continue;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (n + r >= p.N) break;
+        if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at + r] = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
+        else reinterpret_cast<float*>(p.y)[at + r] = acc[i][j][r];
+      }
+    }
+  }
+}
+
 // Launches of a kernel with tiles of bm rows of x and bn of the weight: as many
 // rows of x at once as 2^22 workgroups take.
 template <class F>
@@ -176,9 +516,19 @@ hipError_t launch_rows(const Fp8Product& p, hipStream_t stream) {
   });
 }
 
+template <int BM, int BN, int WM, int WN, bool WIDE>
+hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
+  return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 grid) {
+    hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
+  });
+}
+
 hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
   if (p.M <= 16) return launch_rows<1, 1, 8, 2>(p, stream);
-  return launch_rows<4, 4, 4, 1>(p, stream);
+  if (p.M <= 64) return launch_rows<4, 4, 4, 1>(p, stream);
+  if (!p.bf16) return launch_tile<128, 128, 2, 2, true>(p, stream);
+  if ((p.M + 255) / 256 * ((p.N + 255) / 256) >= 128) return launch_tile<256, 256, 4, 2, false>(p, stream);
+  return launch_tile<128, 128, 2, 2, false>(p, stream);
 }
 
 }  // namespace nvfp4
