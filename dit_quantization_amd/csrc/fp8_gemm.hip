@@ -1,6 +1,7 @@
 // Block-scaled FP8 product y = x^ W^^T (definition: include/fp8.h):
 //   y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{k in b} x[m, k] w[n, k]
 // with b the blocks of 128 columns.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -8,6 +9,8 @@
 #include "lanes.hpp"
 
 namespace nvfp4 {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Four E4M3 values (a dword) as bf16, exact.
 __device__ __forceinline__ u32x2 widen4(uint32_t w) {
@@ -19,6 +22,11 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
   const u32x2 a = widen4(lo), b = widen4(hi);
   return __builtin_bit_cast(bf16x8, u32x4{a.x, a.y, b.x, b.y});
 }
+
+// s_waitcnt immediates (gfx9 encoding): at most n vector memory operations
+// outstanding; all LDS operations complete.
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);
 
 // NaN, infinity, subnormal or zero.
 __device__ __forceinline__ bool not_normal(float v) { return __builtin_amdgcn_classf(v, 0x2F7); }
@@ -36,98 +44,159 @@ __device__ __forceinline__ void add_scaled(f32x4 d, float ws, float xs, f32x4& a
   }
 }
 
+// 16 rows and 128 columns of an operand: a lane has two 16-byte chunks of one
+// row, the same ones of both operands.
+template <bool WIDE>
+struct Fragment8 {
+  u32x4 q[2];
+  __device__ __forceinline__ void load(const u32x4* of, int at0, int at1) {
+    q[0] = of[at0];
+    q[1] = of[at1];
+  }
+  __device__ __forceinline__ i32x8 raw() const {
+    return i32x8{(int)q[0].x, (int)q[0].y, (int)q[0].z, (int)q[0].w, (int)q[1].x, (int)q[1].y, (int)q[1].z, (int)q[1].w};
+  }
+  // the 16 x 16 sums of 128 products, this operand's rows first
+  __device__ __forceinline__ f32x4 times(const Fragment8& o) const {
+    f32x4 d = {0, 0, 0, 0};
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            widen8(q[h / 2][2 * (h & 1)], q[h / 2][2 * (h & 1) + 1]),
+            widen8(o.q[h / 2][2 * (h & 1)], o.q[h / 2][2 * (h & 1) + 1]), d, 0, 0, 0);
+    } else {
+      d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(raw(), o.raw(), d, 0, 0, 0, 0, 0, 0);
+    }
+    return d;
+  }
+};
+
+// Consecutive workgroups go to different XCDs (round robin over 8): the tile
+// for workgroup `bid`, so that each XCD has a contiguous run of tiles.
+__device__ __forceinline__ int xcd_run(int bid, int n) {
+  const int q = n >> 3, r = n & 7, xcd = bid & 7;
+  return xcd * q + min(xcd, r) + (bid >> 3);
+}
+
 // ---- few rows.  A workgroup of W waves has 16 MT rows of x and 16 NT rows of
-// the weight; its waves take the blocks of 128 columns in turn, straight from
-// memory into registers, P blocks ahead, and their sums meet in LDS.  Values
-// are widened to bf16, whose products and sums are fp32's (the FP8 matrix
-// instruction aligns the products of 8 columns to the largest and cuts them
-// off 13 bits below it); memory and not the instruction bounds these calls.
-// Lane l of a 16 x 16 tile feeds row l % 16 and the columns 16 (l / 16) .. + 15
-// and 64 more of a block, the same ones of both operands.  Loads past a row's
-// end or of rows that are not there return zeros.
+// the weight; its waves take runs of P blocks of 128 columns in turn and their
+// sums meet in LDS.  Each wave has P stages of LDS to itself, which it fills
+// straight from memory (8 whole 128-byte lines a load) a run ahead and reads
+// without a barrier.  Values are widened to bf16, whose products and sums are
+// fp32's (the FP8 matrix instruction aligns the products of 8 columns to the
+// largest and cuts them off 13 bits below it); memory and not the instruction
+// bounds these calls.  Loads past a row's end or of rows that are not there
+// return zeros.
 template <int MT, int NT, int W, int P>
 __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
-  constexpr int BM = 16 * MT, BN = 16 * NT;
+  constexpr int BM = 16 * MT, BN = 16 * NT, R = MT + NT;
+  using Fragment = Fragment8<true>;
+  struct Stage {
+    u32x4 x[MT][128], w[NT][128];
+  };
+  union Lds {
+    Stage stages[W][P];
+    f32x4 part[W][MT * NT][64];
+  };
+  __shared__ __attribute__((aligned(16))) Lds lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int tiles_n = (p.N + BN - 1) / BN;
-  const int n0 = (int)(blockIdx.x % (unsigned)tiles_n) * BN;
-  const int64_t m0 = (int64_t)(blockIdx.x / (unsigned)tiles_n) * BM;
+  const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (int)((p.M + BM - 1) / BM);
+  const int bid = xcd_run((int)blockIdx.x, tiles_m * tiles_n);
+  const int n0 = bid / tiles_m * BN;
+  const int64_t m0 = (int64_t)(bid % tiles_m) * BM;
   const int rows = (int)min((int64_t)BM, p.M - m0);
   const int G = (p.K + 127) / 128;
   const __amdgpu_buffer_rsrc_t wbuf =
       make_buf(p.w + (int64_t)n0 * p.K, (uint32_t)min(BN, p.N - n0) * (uint32_t)p.K);
-  const __amdgpu_buffer_rsrc_t xbuf =
-      make_buf(p.x + m0 * p.K, (uint32_t)rows * (uint32_t)p.K);
-  const __amdgpu_buffer_rsrc_t sbuf =
-      make_buf(p.xs + m0 * G, (uint32_t)rows * (uint32_t)G * 4u);
-  const float* ws = p.ws + (int64_t)(n0 / 128) * G;
-  uint32_t w_off[NT], x_off[MT], s_off[MT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) w_off[t] = (uint32_t)(16 * t + l16) * (uint32_t)p.K;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    x_off[t] = (uint32_t)(16 * t + l16) * (uint32_t)p.K;
-    s_off[t] = (uint32_t)min(16 * t + l16, rows - 1) * (uint32_t)G * 4u;
-  }
-  u32x4 wq[P][NT][2], xq[P][MT][2];
-  float xs[P][MT], wsc[P];
-  const auto load = [&](int s, int b) {
+  const __amdgpu_buffer_rsrc_t xbuf = make_buf(p.x + m0 * p.K, (uint32_t)rows * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t sbuf = make_buf(p.xs + m0 * G, (uint32_t)rows * (uint32_t)G * 4u);
+  const auto* ws = (const __attribute__((address_space(4))) float*)p.ws + (int64_t)(n0 / 128) * G;  // (scalar loads)
+  // A load has 8 rows: lane l row l / 8, into slot l % 8 the 16-byte chunk (l %
+  // 8) ^ (row / 2 % 8), so that the reads of 16 rows below meet all banks.
+  const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));  // rows 8 .. 15: ^ 64
+  const uint32_t row_off = (uint32_t)(lane >> 3) * (uint32_t)p.K;
+  Stage* const st = lds.stages[wave];
+  const auto fetch = [&](int s, int b) {
+    const uint32_t k = 128u * (uint32_t)b;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t k = 128u * (uint32_t)b + 64u * h + 16u * (uint32_t)g;
-      const bool ok = k < (uint32_t)p.K;
+      const uint32_t c = k + (chunk ^ (64u * h));
+      // chunks past a row's end: zeros for x, and whatever the next row of the
+      // weight holds (zeros behind the last) for the weight; blocks past the end: zeros
+      const bool x_ok = c < (uint32_t)p.K, w_ok = b < G;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        wq[s][t][h] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, ok ? w_off[t] + k : kBufOOB, 0, 0);
+        buffer_to_lds16(wbuf, st[s].w[t] + 64 * h, w_ok ? row_off + (uint32_t)(16 * t + 8 * h) * (uint32_t)p.K + c : kBufOOB, 0);
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        xq[s][t][h] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, ok ? x_off[t] + k : kBufOOB, 0, 0);
+        buffer_to_lds16(xbuf, st[s].x[t] + 64 * h, x_ok ? row_off + (uint32_t)(16 * t + 8 * h) * (uint32_t)p.K + c : kBufOOB, 0);
     }
-    const int bs = min(b, G - 1);  // a block past the end adds zeros
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-      xs[s][t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, s_off[t] + 4u * (uint32_t)bs, 0, 0));
-    wsc[s] = ws[bs];
   };
+  // scales of a run's blocks (past a row's end whatever the next one holds, or 0: those blocks' sums are 0)
+  static_assert(P == 2 || P == 4, "one load of scales");
+  uint32_t s_off[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) s_off[t] = (uint32_t)min(16 * t + l16, rows - 1) * (uint32_t)G * 4u;
+  typedef float Run __attribute__((ext_vector_type(P)));
+  Run xs[2][MT], wsc[2];
+  const auto fetch_scales = [&](int i, int b) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const uint32_t off = s_off[t] + 4u * (uint32_t)min(b, G - 1);
+      if constexpr (P == 4) xs[i][t] = __builtin_bit_cast(Run, __builtin_amdgcn_raw_buffer_load_b128(sbuf, off, 0, 0));
+      else xs[i][t] = __builtin_bit_cast(Run, __builtin_amdgcn_raw_buffer_load_b64(sbuf, off, 0, 0));
+    }
+#pragma unroll
+    for (int s = 0; s < P; ++s) wsc[i][s] = ws[min(b + s, G - 1)];
+  };
+  // chunks g and g + 4 of a row, the same columns of both operands
+  const int sw = (l16 >> 1) & 7, at0 = 8 * l16 + (g ^ sw), at1 = 8 * l16 + ((g + 4) ^ sw);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+  fetch_scales(0, P * wave);
+  __builtin_amdgcn_sched_barrier(0);  // (these loads are the oldest, so that waiting for them waits for no others)
 #pragma unroll
-  for (int s = 0; s < P; ++s) load(s, wave + W * s);
-  for (int b = wave; b < G; b += W * P) {
+  for (int s = 0; s < P; ++s) fetch(s, P * wave + s);
+  for (int b = P * wave; b < G; b += P * W) {
+    fetch_scales(1, b + P * W);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < P; ++s) {
-      bf16x8 xb[MT][4];
+      // this stage's loads have landed: newer are the other stages', and the next run's scales
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm((P - 1) * 2 * R));
+      __builtin_amdgcn_sched_barrier(0);
+      Fragment xb[MT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) xb[i][h] = widen8(xq[s][i][h / 2][2 * (h & 1)], xq[s][i][h / 2][2 * (h & 1) + 1]);
+      for (int i = 0; i < MT; ++i) xb[i].load(st[s].x[i], at0, at1);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        bf16x8 wb[4];
+        Fragment wb;
+        wb.load(st[s].w[t], at0, at1);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) wb[h] = widen8(wq[s][t][h / 2][2 * (h & 1)], wq[s][t][h / 2][2 * (h & 1) + 1]);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          f32x4 d = {0, 0, 0, 0};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[h], xb[i][h], d, 0, 0, 0);
-          add_scaled(d, wsc[s], xs[s][i], acc[i][t]);
-        }
+        for (int i = 0; i < MT; ++i) add_scaled(wb.times(xb[i]), wsc[0][s], xs[0][i][s], acc[i][t]);
       }
-      load(s, b + W * (s + P));
+      // the stage has been read
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(s, b + P * W + s);
     }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xs[0][t] = xs[1][t];
+    wsc[0] = wsc[1];
   }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS
   // the waves' sums, in wave order
-  __shared__ f32x4 part[W > 1 ? W : 1][MT * NT][64];
   if (W > 1) {
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) part[wave][i * NT + t][lane] = acc[i][t];
+      for (int t = 0; t < NT; ++t) lds.part[wave][i * NT + t][lane] = acc[i][t];
     __syncthreads();
   }
   // a wave finishes the tiles wave, wave + W, ...
@@ -138,9 +207,9 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
       if ((i * NT + t) % W != wave) continue;
       f32x4 v = acc[i][t];
       if (W > 1) {
-        v = part[0][i * NT + t][lane];
+        v = lds.part[0][i * NT + t][lane];
 #pragma unroll
-        for (int u = 1; u < W; ++u) v += part[u][i * NT + t][lane];
+        for (int u = 1; u < W; ++u) v += lds.part[u][i * NT + t][lane];
       }
       // lane: row m of x, four rows n of the weight
       const int m = 16 * i + l16, n = n0 + 16 * t + 4 * g;
@@ -157,25 +226,16 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
 
 // ---- many rows.  A workgroup of WM x WN waves has BM rows of x and BN rows of
 // the weight, a wave TM x TN tiles of 16 x 16.  One step a block of 128
-// columns: both operands' rows go from memory to LDS directly (two stages, one
-// filled while the other is read), 16-byte chunks XOR-swizzled so that the
+// columns: both operands' rows go from memory to LDS directly (NS stages, the others
+// filled while one is read), 16-byte chunks XOR-swizzled so that the
 // fragment reads of 16 rows meet all banks.  The weight is the instruction's
 // first operand, so a lane's results are 4 rows of the weight for one row of
 // x, and one factor xs ws serves them all: a block's sums start from zero in
 // the matrix instruction and are added to the running ones by a multiply-add,
 // which the vector units do while the matrix unit has the next tiles.
 // WIDE: widened to bf16 on the way to the matrix instruction (fp32 outputs).
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// Consecutive workgroups go to different XCDs (round robin over 8): the tile
-// for workgroup `bid`, so that each XCD has a contiguous run of tiles.
-__device__ __forceinline__ int xcd_run(int bid, int n) {
-  const int q = n >> 3, r = n & 7, xcd = bid & 7;
-  return xcd * q + min(xcd, r) + (bid >> 3);
-}
-
-template <int BM, int BN, int WM, int WN, bool WIDE>
-__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2))) void fp8_gemm_tile_kernel(Fp8Product p) {
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_tile_kernel(Fp8Product p) {
   constexpr int NT = WM * WN * 64, NW = WM * WN;
   constexpr int WBM = BM / WM, WBN = BN / WN;        // a wave's tile
   constexpr int TM = WBM / 16, TN = WBN / 16;
@@ -185,8 +245,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
   static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && WD % 2 == 0 && XSW < NW && TN % 4 == 0, "tile and waves");
   static_assert(128 % WBN == 0, "a wave's rows of the weight share a scale");
   struct Stages {
-    u32x4 x[2][BM * 8], w[2][BN * 8];
-    f32x4 scales[2][NW * 64], unused[NW * 64];  // of 4 blocks a row
+    u32x4 x[NS][BM * 8], w[NS][BN * 8];
+    f32x4 scales[2][(XSW + 1) * 64], unused[64];  // of 4 blocks a row
   };
   __shared__ __attribute__((aligned(16))) Stages st;
 
@@ -245,11 +305,12 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
     }
   };
   // The scales of the 4 blocks from b on, a row 16 bytes (past a row's end
-  // whatever the next one holds), every fourth time; in between the load
-  // fetches nothing and goes nowhere.
+  // whatever the next one holds), every fourth time; in between, and in the
+  // waves behind, the load fetches nothing and goes nowhere.
+  static_assert(NS <= 5, "a block's scales are read before those of the block 8 later come");
   const auto dma_scales = [&](int b) {
-    const bool due = (b & 3) == 0 && b < G;
-    buffer_to_lds16(scbuf, reinterpret_cast<u32x4*>((due ? st.scales[(b >> 2) & 1] : st.unused) + 64 * wave),
+    const bool due = ((b & 3) == 0) & (b < G) & (wave <= XSW);  // (no branches: they would split the step)
+    buffer_to_lds16(scbuf, reinterpret_cast<u32x4*>(due ? st.scales[(b >> 2) & 1] + 64 * wave : st.unused),
                     due ? sc_off : kBufOOB, 4u * (uint32_t)min(b, G - 1));
   };
 
@@ -257,11 +318,11 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
   const int sw = (l16 >> 1) & 7;
   const int x_row = (wm * WBM + l16) * 8, w_row = (wn * WBN + l16) * 8;
   const int x0 = x_row + (g ^ sw), x1 = x_row + ((g + 4) ^ sw), w0 = w_row + (g ^ sw), w1 = w_row + ((g + 4) ^ sw);
-  u32x4 xf[TM][2], wf[WB][2];
+  Fragment8<WIDE> xf[TM], wf[WB];
   float s[TM], xsc[TM], wsc, s_last = 0.0f;
   bool odd = false;
-  const auto load_x = [&](int stage, int j, int h) { xf[j][h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
-  const auto load_w = [&](int stage, int i, int h) { wf[i % WB][h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
+  const auto load_x = [&](int stage, int j, int h) { xf[j].q[h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
+  const auto load_w = [&](int stage, int i, int h) { wf[i % WB].q[h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
   const auto load_scales = [&](int b) {
     const float* of = reinterpret_cast<const float*>(st.scales[(b >> 2) & 1]) + (b & 3);
 #pragma unroll
@@ -285,21 +346,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
 #pragma unroll
     for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  const auto multiply = [&](int i, int j) {
-    const u32x4 *a = wf[i % WB], *b = xf[j];
-    f32x4 d = {0, 0, 0, 0};
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(a[h / 2][2 * (h & 1)], a[h / 2][2 * (h & 1) + 1]),
-                                                    widen8(b[h / 2][2 * (h & 1)], b[h / 2][2 * (h & 1) + 1]), d, 0, 0, 0);
-    } else {
-      const i32x8 av = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
-      const i32x8 bv = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
-      d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, d, 0, 0, 0, 0, 0, 0);
-    }
-    return d;
-  };
+  const auto multiply = [&](int i, int j) { return wf[i % WB].times(xf[j]); };
   // Tile q of a step: rows 0 .. TN - LAST - 1, then the columns of the last
   // rows.  A tile's sums are added two tiles later, while the matrix unit has
   // the next ones (the first two of a step add the last two of the step before).
@@ -327,32 +374,32 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
   };
   // A step meets twice: in front of row A, from which on the second half of
   // the weight's rows is read, all waves have block b's x and first half in
-  // registers, so block b + 2's go into their place; in front of the last
+  // registers, so block b + NS's go into their place; in front of the last
   // rows the same for the second half, and block b + 1's x and first half are
-  // there.  Every load has one and a half steps to land.
+  // there.  Every load has NS - 1/2 steps to land.
   constexpr int A = TN / 2 - 2;
   constexpr int SLACK = L1 + 1 + L2;  // loads of a block, one for scales among them
+  static_assert((NS - 1) * SLACK + L2 <= 63, "the counter of loads in flight");
   const auto step = [&](int b, int cur) {
-    const int nxt = cur ^ 1;
+    const int nxt = (cur + 1) % NS;
 #pragma unroll
     for (int q = 0; q < T0; ++q) {
       const int i = q / TM, c = q % TM;
-      if (q == A * TM) meet(std::integral_constant<int, SLACK>{});
+      if (q == A * TM) meet(std::integral_constant<int, (NS - 1) * SLACK>{});
       if (c < 2) load_w(cur, i + 2, c);
-      if (q >= A * TM && q - A * TM < L1) dma(cur, b + 2, q - A * TM);
-      if (q == T0 - 1) dma_scales(b + 2);
+      if (q >= A * TM && q - A * TM < L1) dma(cur, b + NS, q - A * TM);
+      if (q == T0 - 1) dma_scales(b + NS);
       tile(q);
       __builtin_amdgcn_sched_barrier(0);
     }
-    static_assert(T0 - A * TM >= L1 || TM == 2, "");
 #pragma unroll
-    for (int q = T0 - A * TM; q < L1; ++q) dma(cur, b + 2, q);
-    meet(std::integral_constant<int, SLACK>{});
+    for (int q = T0 - A * TM; q < L1; ++q) dma(cur, b + NS, q);
+    meet(std::integral_constant<int, (NS - 1) * SLACK>{});
     load_scales(b + 1);
 #pragma unroll
     for (int q = T0; q < TILES; ++q) {
       const int c = (q - T0) / LAST, in_c = (q - T0) % LAST;
-      if (q - T0 < L2) dma(cur, b + 2, L1 + q - T0);
+      if (q - T0 < L2) dma(cur, b + NS, L1 + q - T0);
       tile(q);
       if (q - T0 < 4) load_w(nxt, (q - T0) / 2, (q - T0) % 2);
       if (in_c == LAST - 1) {
@@ -362,21 +409,21 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int q = TILES - T0; q < L2; ++q) dma(cur, b + 2, L1 + q);
+    for (int q = TILES - T0; q < L2; ++q) dma(cur, b + NS, L1 + q);
     s_last = s[TM - 1];
     factors();
   };
   static_assert(TM >= 2, "a tile a fragment's load");
 
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < NS; ++b) {
 #pragma unroll
     for (int q = 0; q < L1; ++q) dma(b, b, q);
     dma_scales(b);
 #pragma unroll
     for (int q = L1; q < L1 + L2; ++q) dma(b, b, q);
   }
-  meet(std::integral_constant<int, SLACK + L2>{});
+  meet(std::integral_constant<int, (NS - 1) * SLACK + L2>{});
   load_scales(0);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -387,11 +434,23 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
   }
   factors();
   int b = 0;
-  for (; b + 2 <= G; b += 2) {
+  for (; b + NS <= G; b += NS) {
     step(b, 0);
     step(b + 1, 1);
+    if constexpr (NS > 2) step(b + 2, 2);
+    if constexpr (NS > 3) step(b + 3, 3);
+    if constexpr (NS > 4) step(b + 4, 4);
   }
   if (b < G) step(b, 0);
+  if constexpr (NS > 2) {
+    if (b + 1 < G) step(b + 1, 1);
+  }
+  if constexpr (NS > 3) {
+    if (b + 2 < G) step(b + 2, 2);
+  }
+  if constexpr (NS > 4) {
+    if (b + 3 < G) step(b + 3, 3);
+  }
 #pragma unroll
   for (int q = TILES - LAG; q < TILES; ++q) add(q, s_last);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
@@ -421,10 +480,10 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)
         }
       };
 #pragma unroll
-      for (int j = 0; j < TM; ++j) fragment(xbuf, wm * WBM + 16 * j + l16, xf[j]);
+      for (int j = 0; j < TM; ++j) fragment(xbuf, wm * WBM + 16 * j + l16, xf[j].q);
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
-        fragment(wbuf, wn * WBN + 16 * i + l16, wf[i % WB]);
+        fragment(wbuf, wn * WBN + 16 * i + l16, wf[i % WB].q);
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
           const f32x4 e = multiply(i, j);
@@ -516,19 +575,48 @@ hipError_t launch_rows(const Fp8Product& p, hipStream_t stream) {
   });
 }
 
-template <int BM, int BN, int WM, int WN, bool WIDE>
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
 hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
   return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 grid) {
-    hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
+    hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, NS, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
   });
 }
 
+// Few rows in all: workgroups of few waves that share nothing but their sums,
+// as long as there are about two of them a CU at most; from there on tiles
+// through LDS, by their estimated time.
+// (us, K = 4096: M = 16, N = 1024 / 4096 / 14336: rows<1, 1> 4.6 / 6.4 / 17.0, rows<1, 2> 5.7 / 7.5 (8 waves), - / - / 14.6
+// (4); M = 32, N = 4096: rows<2, 1> 7.8, rows<2, 2> 9.9; M = 64, N = 4096: rows<2, 2> of 8 waves 9.8, of 4 10.4, 64 x 64 tiles
+// 15.6; M = 128, N = 4096: 17.0, 14.3, 15.7; M = 64, N = 14336: rows<2, 2> 27.9, 64 x 64 tiles 17.2.)
 hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
-  if (p.M <= 16) return launch_rows<1, 1, 8, 2>(p, stream);
-  if (p.M <= 64) return launch_rows<4, 4, 4, 1>(p, stream);
-  if (!p.bf16) return launch_tile<128, 128, 2, 2, true>(p, stream);
-  if ((p.M + 255) / 256 * ((p.N + 255) / 256) >= 128) return launch_tile<256, 256, 4, 2, false>(p, stream);
-  return launch_tile<128, 128, 2, 2, false>(p, stream);
+  const auto tiles = [&](int64_t bm, int64_t bn) { return (p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
+  if (p.M <= 16) {
+    if (tiles(16, 16) <= 512) return launch_rows<1, 1, 8, 2>(p, stream);
+    return launch_rows<1, 2, 4, 2>(p, stream);
+  }
+  const int64_t t = tiles(32, 16);
+  if (t <= 256) return launch_rows<2, 1, 4, 4>(p, stream);
+  if (t <= 512) return launch_rows<2, 2, 8, 2>(p, stream);
+  if (t <= 1024) return launch_rows<2, 2, 4, 2>(p, stream);
+  // Time of a step (a block of 128 columns of all tiles), in us: that of the
+  // rounds of workgroups that the 256 CUs take, one or two a CU; measured at K =
+  // 4096 and 14336 on M = 64 .. 4096, N = 1024 .. 14336.
+  const auto one = [&](int bm, int bn, double us) { return (double)((tiles(bm, bn) + 255) / 256) * us; };
+  const auto two = [&](int bm, int bn, double alone, double both) {
+    return tiles(bm, bn) <= 256 ? alone : (double)((tiles(bm, bn) + 511) / 512) * both;
+  };
+  if (!p.bf16) {
+    if (two(64, 128, 0.8, 1.3) < two(128, 128, 1.2, 2.0)) return launch_tile<64, 128, 2, 2, 2, true>(p, stream);
+    return launch_tile<128, 128, 2, 2, 2, true>(p, stream);
+  }
+  const double t64 = two(64, 64, 0.47, 0.66), t64x128 = two(64, 128, 0.53, 0.95), t128 = two(128, 128, 0.73, 1.25),
+               t128x256 = one(128, 256, 1.15), t256 = one(256, 256, 1.9);
+  const double best = std::min({t64, t64x128, t128, t128x256, t256});
+  if (best == t256) return launch_tile<256, 256, 4, 2, 2, false>(p, stream);
+  if (best == t128x256) return launch_tile<128, 256, 2, 4, 3, false>(p, stream);
+  if (best == t128) return launch_tile<128, 128, 2, 2, 2, false>(p, stream);
+  if (best == t64x128) return launch_tile<64, 128, 2, 2, 3, false>(p, stream);
+  return launch_tile<64, 64, 2, 1, 4, false>(p, stream);
 }
 
 }  // namespace nvfp4

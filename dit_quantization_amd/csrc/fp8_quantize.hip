@@ -78,11 +78,38 @@ hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t
 // ---- activations.  A row is cut into slots of 8 columns, filled up to whole
 // groups, and slots go to threads in order, so that a group is 4, 8 or 16
 // neighbouring lanes.
+
+// g / (1 + exp(-g)) to within 2^-45 of itself: exp(-g) = 2^n exp(r), |r| <= ln 2
+// / 2, by 12 terms of its series (the rest is below 2^-47), and a reciprocal of
+// the hardware's estimate (23 bits) and one Newton step.  g beyond 700 counts as
+// 700 in the exponential: the product is below 10^-260, or g, either way.
+__device__ __forceinline__ double silu64(float g) {
+  constexpr double kMagic = 6755399441055744.0;  // 1.5 2^52: leaves the nearest integer in the low bits
+  constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
+  const double z = (double)g, v = -(double)__builtin_amdgcn_fmed3f(g, -700.0f, 700.0f);
+  const double m = __builtin_fma(v, kLog2e, kMagic);
+  const double r = __builtin_fma(m - kMagic, -kLn2, v);
+  double e = 1.0 / 39916800.0;
+  constexpr double kInv[11] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                               1.0 / 362880, 1.0 / 3628800};
+#pragma unroll
+  for (int i = 10; i >= 0; --i) e = __builtin_fma(e, r, kInv[i]);
+  const double d = 1.0 + __builtin_amdgcn_ldexp(e, (int)__double_as_longlong(m));
+  const double q = __builtin_amdgcn_rcp(d);
+  return z * __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
+}
+
 template <bool BF, bool SILU>
-__global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, double q) {
-  const uint64_t at = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = (int64_t)(at / slots);
-  const int i = (int)(at % slots), c = 8 * i;
+__global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, uint32_t per, double q) {
+  // at / slots, per = 2^32 / slots rounded down: the first quotient is exact or one short
+  const uint32_t at = blockIdx.x * 256 + threadIdx.x;
+  uint32_t row = __umulhi(at, per), i = at - row * slots;
+  if (i >= slots) {
+    ++row;
+    i -= slots;
+  }
+  const int64_t r = row;
+  const int c = 8 * (int)i;
   const bool live = r < a.rows && c < a.cols;
   Vec8<BF> x, g;
   x.zero();
@@ -95,10 +122,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     y[j] = (double)x.at(j);
-    if (SILU) {
-      const double v = (double)g.at(j);
-      y[j] *= v / (1.0 + exp(-v));
-    }
+    if (SILU) y[j] *= silu64(g.at(j));
     top = fmax(top, fabs(y[j]));
   }
   const int L = a.group / 8;
@@ -113,6 +137,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32
 hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
   const int L = all.group / 8;
   const uint32_t slots = (uint32_t)((all.cols + all.group - 1) / all.group * L);
+  const uint32_t per = (uint32_t)(((uint64_t)1 << 32) / slots);  // slots >= 4
   // at most 2^31 threads a launch, whole rows
   const int64_t step = ((int64_t)1 << 31) / slots;
   for (int64_t r0 = 0; r0 < all.rows; r0 += step) {
@@ -126,7 +151,7 @@ hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
     const dim3 grid((unsigned)((a.rows * slots + 255) / 256));
     const double q = a.e4m3 ? 448.0 : 127.0;
 #define ACT_CASE(BF, SILU) \
-  hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU>), grid, dim3(256), 0, stream, a, slots, q)
+  hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU>), grid, dim3(256), 0, stream, a, slots, per, q)
     if (a.gate && a.bf16) ACT_CASE(true, true);
     else if (a.gate) ACT_CASE(false, true);
     else if (a.bf16) ACT_CASE(true, false);
