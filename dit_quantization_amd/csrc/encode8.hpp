@@ -132,6 +132,28 @@ __device__ __forceinline__ u32x2 encode_quotients(const double v[8], float s, bo
   return e4m3 ? encode_e4m3(q, 1.0) : encode_i8(q, 1.0);
 }
 
+// 8 codes of exact fp32 or bf16 values v / s.  INT8 in fp32 unless a quotient is
+// next to half way between two codes (or the scale is next to the end of fp32's
+// range).
+template <bool BF16>
+__device__ __forceinline__ u32x2 encode(const Vec8<BF16>& v, float s, bool e4m3) {
+  bool exact = e4m3 || s < 0x1p-120f;
+  u32x2 q;
+  if (!e4m3) {
+    float p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = v.at(j);
+    q = encode_i8_fast(p, (float)rcp64((double)s), exact);
+  }
+  if (exact) {
+    double d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) d[j] = (double)fresh(v.at(j));
+    q = encode_quotients(d, s, e4m3);
+  }
+  return q;
+}
+
 // fp32(top / Q), 1 where that is 0.
 __device__ __forceinline__ float scale_for(double top, double q) {
   const float s = (float)(top / q);

@@ -1,5 +1,9 @@
 // Paged 8-bit caches of keys and values: quantized as they are written, and
 // read back (definitions: include/kvcache.h).
+//
+// A workgroup has some tokens of one of the two tensors.  First a thread a
+// token finds its place (a search in cu and one page number), then all threads
+// move the tokens' heads, several vectors in flight each.
 #include "device_common.hpp"
 #include "encode8.hpp"
 #include "fp8_kernels.hpp"
@@ -7,126 +11,210 @@
 
 namespace nvfp4 {
 
-enum class Place { kHeld, kNowhere, kNoSequence };
+constexpr int kMaxTokens = 256;  // of a workgroup
 
-// Where row t belongs: page and row in the page.
-__device__ __forceinline__ Place locate(const kv8_places& p, int64_t t, int64_t& page, int64_t& row) {
-  int lo = 0, hi = (int)p.seqs;
-  if (t < p.cu[0] || t >= p.cu[hi]) return Place::kNoSequence;
-  while (hi - lo > 1) {  // cu[lo] <= t < cu[hi]
-    const int mid = lo + (hi - lo) / 2;
-    if (p.cu[mid] <= t) lo = mid;
-    else hi = mid;
+// Where a token is: page and row in the page; page -1 where it has no place,
+// -2 where it belongs to no sequence.
+struct Place {
+  int page, row;
+};
+struct Places {
+  Place at[kMaxTokens];
+  int cu[257];  // every step-th entry of the table, so that 256 or fewer sequences are searched in LDS
+};
+
+__device__ __forceinline__ Place locate(const kv8_places& p, const int* cu, int step, int64_t t) {
+  if (t < cu[0] || t >= cu[256]) return {-2, 0};
+  int lo = 0;
+#pragma unroll
+  for (int half = 128; half > 0; half /= 2) lo += cu[lo + half] <= t ? half : 0;  // cu[lo] <= t < cu[lo + half]
+  int first = cu[lo];
+  if (step > 1) {
+    lo *= step;
+    int hi = min(lo + step, (int)p.seqs);
+    while (hi - lo > 1) {  // p.cu[lo] <= t < p.cu[hi]
+      const int mid = lo + (hi - lo) / 2, v = p.cu[mid];
+      if (v <= t) lo = mid, first = v;
+      else hi = mid;
+    }
   }
-  const int64_t at = t - p.cu[lo] + (p.starts ? p.starts[lo] : 0);
-  if (at < 0) return Place::kNowhere;
-  const int64_t slot = at / p.page_size;
-  if (slot >= p.table_width) return Place::kNowhere;
-  page = p.page_table[lo * p.table_width + slot];
-  row = at - slot * p.page_size;
-  return page >= 0 && page < p.pages ? Place::kHeld : Place::kNowhere;
+  const int64_t at = t - first + (p.starts ? p.starts[lo] : 0);
+  if (at < 0 || at >= p.table_width * p.page_size) return {-1, 0};
+  const uint32_t slot = (uint32_t)at / (uint32_t)p.page_size;  // at < 2^32
+  const int page = p.page_table[lo * p.table_width + slot];
+  return {page >= 0 && page < p.pages ? page : -1, (int)((uint32_t)at - slot * (uint32_t)p.page_size)};
 }
 
-// A row is one token and head; T lanes have it, V vectors of 8 elements each.
-template <bool BF, int T, int V>
-__global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3) {
+// The places of this workgroup's tokens t0, t0 + 1, ..., and how many it has.
+__device__ __forceinline__ int locate_all(const kv8_places& p, int64_t t0, int per_block, Places& places) {
+  const int n = (int)min((int64_t)per_block, p.tokens - t0), k = threadIdx.x;
+  const int step = (int)((p.seqs + 255) / 256);
+  places.cu[k] = p.cu[min((int64_t)k * step, p.seqs)];
+  if (k == 0) places.cu[256] = p.cu[p.seqs];
+  __syncthreads();
+  if (k < n) places.at[k] = locate(p, places.cu, step, t0 + k);
+  __syncthreads();
+  return n;
+}
+
+// a / b for a < 2^31, with per = 2^32 / b rounded down (b > 1).
+__device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b, uint32_t per) {
+  if (b == 1) return a;
+  const uint32_t q = __umulhi(a, per);  // exact or one short
+  return q + (a - q * b >= b ? 1 : 0);
+}
+
+// A row is one token and head; T lanes have it, V vectors of 8 elements each,
+// and U rows at a time.
+template <bool BF, int T, int V, int U>
+__global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3,
+                                                        int64_t first, int per_block, uint32_t per_head) {
+  __shared__ Places places;
   const kv8_tensor& c = blockIdx.y ? values : keys;
+  const int64_t t0 = first + (int64_t)blockIdx.x * per_block;
+  const int n = locate_all(p, t0, per_block, places) * (int)p.heads;
   const int lane = threadIdx.x % T;
-  const int64_t all = p.tokens * p.heads, step = (int64_t)gridDim.x * (256 / T);
-  for (int64_t i = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T; i < all; i += step) {
-    const int64_t t = i / p.heads, h = i - t * p.heads;
-    int64_t page, row;
-    if (locate(p, t, page, row) != Place::kHeld) continue;  // the same for the T lanes
-    Vec8<BF> v[V];
-    float top = 0.0f;
+  for (int i0 = threadIdx.x / T; i0 < n; i0 += U * (256 / T)) {
+    Vec8<BF> v[U][V];
+    uint8_t* codes[U];
+    float* scale[U];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j].zero();
-      const int e = 8 * (lane + T * j);
-      if (e < c.dim) v[j].load(c.rows, t * c.token_stride + h * c.head_stride + e);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * (256 / T);
+      codes[u] = nullptr;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[j].at(k)));
-    }
-    const auto most = [](float a, float b) { return fmaxf(a, b); };
-    top = lanes_all<(T > 16 ? 16 : T)>(top, most);
-    if (T >= 32) top = most(top, __shfl_xor(top, 16));
-    if (T >= 64) top = most(top, __shfl_xor(top, 32));
-    const float s = scale_for((double)top, e4m3 ? 448.0 : 127.0);
-    const int64_t at = row * p.heads + h;
-    if (lane == 0) c.scales[page * c.scale_stride + at] = s;
-    uint8_t* codes = reinterpret_cast<uint8_t*>(c.codes) + page * c.code_stride + at * c.dim;
+      for (int j = 0; j < V; ++j) v[u][j].zero();
+      if (i < n) {
+        const int t = (int)divide((uint32_t)i, (uint32_t)p.heads, per_head), h = i - t * (int)p.heads;
+        const Place at = places.at[t];
+        if (at.page >= 0) {  // the same for the T lanes
+          const int64_t row = (int64_t)at.row * p.heads + h;
+          codes[u] = reinterpret_cast<uint8_t*>(c.codes) + at.page * c.code_stride + row * c.dim;
+          scale[u] = c.scales + at.page * c.scale_stride + row;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int e = 8 * (lane + T * j);
-      double d[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = (double)v[j].at(k);
-      if (e < c.dim) *reinterpret_cast<u32x2*>(codes + e) = encode_quotients(d, s, e4m3);
-    }
-  }
-}
-
-// A thread has 16 elements of a row.
-template <bool BF>
-__global__ __launch_bounds__(256) void kv8_read_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3) {
-  const kv8_tensor& c = blockIdx.y ? values : keys;
-  const int64_t per = c.dim / 16, all = p.tokens * p.heads * per, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-    const int64_t u = i / per, t = u / p.heads, h = u - t * p.heads, e = 16 * (i - u * per);
-    int64_t page, row;
-    const Place place = locate(p, t, page, row);
-    if (place == Place::kNoSequence) continue;
-    float v[16] = {};
-    if (place == Place::kHeld) {
-      const int64_t at = row * p.heads + h;
-      const float s = c.scales[page * c.scale_stride + at];
-      const u32x4 q =
-          *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(c.codes) + page * c.code_stride + at * c.dim + e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (e4m3) {
-          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q[j], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q[j], true);
-          v[4 * j] = a.x * s, v[4 * j + 1] = a.y * s, v[4 * j + 2] = b.x * s, v[4 * j + 3] = b.y * s;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int8_t)(q[j] >> (8 * k)) * s;
+          for (int j = 0; j < V; ++j) {
+            const int e = 8 * (lane + T * j);
+            if (e < c.dim) v[u][j].load(c.rows, (t0 + t) * c.token_stride + h * c.head_stride + e);
+          }
         }
       }
     }
-    const int64_t at = t * c.token_stride + h * c.head_stride + e;
-    Vec8<BF> o;
-    o.set(v);
-    o.store(c.rows, at);
-    o.set(v + 8);
-    o.store(c.rows, at + 8);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!codes[u]) continue;
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[u][j].at(k)));
+      const auto most = [](float a, float b) { return fmaxf(a, b); };
+      top = lanes_all<(T > 16 ? 16 : T)>(top, most);
+      if (T >= 32) top = most(top, __shfl_xor(top, 16));
+      if (T >= 64) top = most(top, __shfl_xor(top, 32));
+      const float s = scale_for((double)top, e4m3 ? 448.0 : 127.0);
+      if (lane == 0) *scale[u] = s;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = 8 * (lane + T * j);
+        if (e < c.dim) *reinterpret_cast<u32x2*>(codes[u] + e) = encode(v[u][j], s, e4m3);
+      }
+    }
+  }
+}
+
+// A thread has 16 elements of a head, U times.
+template <bool BF, int U>
+__global__ __launch_bounds__(256) void kv8_read_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3,
+                                                       int64_t first, int per_block, uint32_t per_k, uint32_t per_v, uint32_t per_head) {
+  __shared__ Places places;
+  const kv8_tensor& c = blockIdx.y ? values : keys;
+  const uint32_t units = (uint32_t)c.dim / 16, per_unit = blockIdx.y ? per_v : per_k;
+  const int64_t t0 = first + (int64_t)blockIdx.x * per_block;
+  const uint32_t n = (uint32_t)locate_all(p, t0, per_block, places) * (uint32_t)p.heads * units;
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += 256 * U) {
+    u32x4 q[U];
+    float s[U];
+    int64_t at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + 256 * u;
+      q[u] = u32x4{0, 0, 0, 0};  // no place: zeros
+      s[u] = 0.0f;
+      at[u] = -1;
+      if (i < n) {
+        const uint32_t head = divide(i, units, per_unit), t = divide(head, (uint32_t)p.heads, per_head);
+        const uint32_t h = head - t * (uint32_t)p.heads, e = 16 * (i - head * units);
+        const Place place = places.at[t];
+        if (place.page != -2) at[u] = (t0 + t) * c.token_stride + h * c.head_stride + e;
+        if (place.page >= 0) {
+          const int64_t row = (int64_t)place.row * p.heads + h;
+          s[u] = c.scales[place.page * c.scale_stride + row];
+          q[u] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(c.codes) + place.page * c.code_stride +
+                                                 row * c.dim + e);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at[u] < 0) continue;
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (e4m3) {
+          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], true);
+          v[4 * j] = a.x * s[u], v[4 * j + 1] = a.y * s[u], v[4 * j + 2] = b.x * s[u], v[4 * j + 3] = b.y * s[u];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[4 * j + k] = (float)(int8_t)(q[u][j] >> (8 * k)) * s[u];
+        }
+      }
+      Vec8<BF> o;
+      o.set(v);
+      o.store(c.rows, at[u]);
+      o.set(v + 8);
+      o.store(c.rows, at[u] + 8);
+    }
   }
 }
 
 hipError_t launch_kv8(const kv8_tensor& keys, const kv8_tensor& values, const kv8_places& p, bool bf16, bool e4m3,
                       bool write, hipStream_t stream) {
   const int64_t dim = keys.dim > values.dim ? keys.dim : values.dim;
-  const auto grid = [](int64_t blocks) { return dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), 2); };
+  const auto per = [](int64_t d) { return d > 1 ? (uint32_t)(((uint64_t)1 << 32) / (uint64_t)d) : 0u; };
+  const uint32_t per_head = per(p.heads);
+  // Vectors a thread moves at a time: 4 where there are enough for 4 workgroups
+  // a CU, otherwise 1; a workgroup has as many tokens as give its threads those
+  // (at most 2^22 workgroups a launch, which counts its threads in 32 bits).
+  const auto launch = [&](int64_t vectors_of_token, auto kernel) {
+    const int64_t all = p.tokens * vectors_of_token;
+    const int u = all >= 4 * 256 * 1024 ? 4 : 1;
+    const int64_t fit = 256 * u / vectors_of_token;
+    const int n = (int)(fit < 1 ? 1 : fit > kMaxTokens ? kMaxTokens : fit);
+    const int64_t step = (int64_t)n << 22;
+    for (int64_t first = 0; first < p.tokens; first += step) {
+      const int64_t blocks = ((p.tokens - first < step ? p.tokens - first : step) + n - 1) / n;
+      kernel(dim3((unsigned)blocks, 2), u, first, n);
+      if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  };
   if (!write) {
-    const dim3 g = grid((p.tokens * p.heads * (dim / 16) + 255) / 256);
-    if (bf16) hipLaunchKernelGGL(kv8_read_kernel<true>, g, dim3(256), 0, stream, keys, values, p, e4m3);
-    else hipLaunchKernelGGL(kv8_read_kernel<false>, g, dim3(256), 0, stream, keys, values, p, e4m3);
-    return hipGetLastError();
+    return launch(p.heads * (dim / 16), [&](dim3 g, int u, int64_t first, int n) {
+#define READ_CASE(BF, U)                                                                                          hipLaunchKernelGGL((kv8_read_kernel<BF, U>), g, dim3(256), 0, stream, keys, values, p, e4m3, first, n,                             per(keys.dim / 16), per(values.dim / 16), per_head)
+      if (bf16 && u == 4) READ_CASE(true, 4);
+      else if (bf16) READ_CASE(true, 1);
+      else if (u == 4) READ_CASE(false, 4);
+      else READ_CASE(false, 1);
+#undef READ_CASE
+    });
   }
-#define WRITE_CASE(T, V)                                                                                             \
-  do {                                                                                                               \
-    const dim3 g = grid((p.tokens * p.heads + 256 / T - 1) / (256 / T));                                             \
-    if (bf16)                                                                                                        \
-      hipLaunchKernelGGL((kv8_write_kernel<true, T, V>), g, dim3(256), 0, stream, keys, values, p, e4m3);            \
-    else                                                                                                             \
-      hipLaunchKernelGGL((kv8_write_kernel<false, T, V>), g, dim3(256), 0, stream, keys, values, p, e4m3);           \
-  } while (0)
-  if (dim <= 64) WRITE_CASE(8, 1);
-  else if (dim <= 128) WRITE_CASE(16, 1);
-  else if (dim <= 256) WRITE_CASE(32, 1);
-  else if (dim <= 512) WRITE_CASE(64, 1);
-  else WRITE_CASE(64, 2);
+#define WRITE_CASE(T, V)                                                                                          launch(p.heads * T, [&](dim3 g, int u, int64_t first, int n) {                                                    const auto kernel = bf16 ? u == 4 ? kv8_write_kernel<true, T, V, 4> : kv8_write_kernel<true, T, V, 1>                                    : u == 4 ? kv8_write_kernel<false, T, V, 4> : kv8_write_kernel<false, T, V, 1>;        hipLaunchKernelGGL(kernel, g, dim3(256), 0, stream, keys, values, p, e4m3, first, n, per_head);               })
+  if (dim <= 64) return WRITE_CASE(8, 1);
+  if (dim <= 128) return WRITE_CASE(16, 1);
+  if (dim <= 256) return WRITE_CASE(32, 1);
+  if (dim <= 512) return WRITE_CASE(64, 1);
+  return WRITE_CASE(64, 2);
 #undef WRITE_CASE
-  return hipGetLastError();
 }
 
 }  // namespace nvfp4

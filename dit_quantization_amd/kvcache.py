@@ -70,58 +70,53 @@ def new(pages, page_size, heads, dim, value_dim=None, dtype=torch.int8, device="
     return tuple(out)
 
 
-def _page_stride(t, what):
-    """Elements from page to page of a tensor whose pages are contiguous."""
-    page = 1
+def _page_stride(t, page, what):
+    """Elements from page to page of a tensor of pages of `page` elements, which are contiguous."""
+    if t.is_contiguous():
+        return page
+    inner = 1
     for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
-        if size > 1 and stride != page:
+        if size > 1 and stride != inner:
             raise ValueError(f"{what}: only the first dimension may be strided")
-        page *= size
+        inner *= size
     return t.stride(0) if t.shape[0] > 1 else page
 
 
-def _cache(cache):
-    """(code of its type, pages, page size, heads, the two tensors' fields) of a cache, whose tensors have to agree."""
+def _call(fn, cache, rows, page_table, cu, starts):
+    """Checks a cache, rows of keys and values [tokens, heads, dim] and the tables, and calls fn."""
     kc, ks, vc, vs = cache
-    qt = _i4._code(_i4._BYTES, kc.dtype, "cache")
-    if kc.dim() != 4 or vc.dim() != 4 or vc.dtype != kc.dtype or kc.shape[:3] != vc.shape[:3]:
-        raise ValueError("a cache's codes are two tensors [pages, page_size, heads, dim] of one type that agree but for "
-                         f"dim; got {kc.dtype} {tuple(kc.shape)}, {vc.dtype} {tuple(vc.shape)}")
-    for s in (ks, vs):
-        if s.dtype != torch.float32 or s.shape != kc.shape[:3]:
-            raise ValueError(f"a cache's scales are float32 tensors of shape {tuple(kc.shape[:3])}; got {s.dtype} "
+    qt = _i4._BYTES.get(kc.dtype)
+    if qt is None or kc.dim() != 4 or vc.dim() != 4 or vc.dtype != kc.dtype or kc.shape[:3] != vc.shape[:3]:
+        raise ValueError("a cache's codes are two int8 or float8_e4m3fn tensors [pages, page_size, heads, dim] that agree "
+                         f"but for dim; got {kc.dtype} {tuple(kc.shape)}, {vc.dtype} {tuple(vc.shape)}")
+    dt = rows[0].dtype
+    tokens = rows[0].shape[0]
+    pages, size, heads, _ = kc.shape
+    tensors = []
+    for c, s, t, what in ((kc, ks, rows[0], "keys"), (vc, vs, rows[1], "values")):
+        dim = c.shape[3]
+        if s.dtype != torch.float32 or s.shape != c.shape[:3]:
+            raise ValueError(f"a cache's scales are float32 tensors of shape {tuple(c.shape[:3])}; got {s.dtype} "
                              f"{tuple(s.shape)}")
-    fields = [(c.data_ptr(), s.data_ptr(), _page_stride(c, "codes"), _page_stride(s, "scales"))
-              for c, s in ((kc, ks), (vc, vs))]
-    return qt, kc.shape, fields
-
-
-def _rows(t, shape, dtype, what):
-    """(token stride, head stride) of rows [tokens, heads, dim]."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}; got {t.dtype} {tuple(t.shape)}")
-    if t.stride(2) != 1 and t.shape[2] > 1:
-        raise ValueError(f"{what}'s heads must be contiguous")
-    return t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
-
-
-def _call(fn, cache, described, k, v, page_table, cu, starts):
-    qt, (pages, size, heads, _), fields = described
+        if t.shape != (tokens, heads, dim) or t.dtype != dt:
+            raise ValueError(f"{what} must be a {dt} tensor of shape {(tokens, heads, dim)}; got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        token, head, one = t.stride()
+        if one != 1 and dim > 1:
+            raise ValueError(f"{what}'s heads must be contiguous")
+        tensors.append(Tensor(c.data_ptr(), s.data_ptr(), _page_stride(c, size * heads * dim, "codes"),
+                              _page_stride(s, size * heads, "scales"), t.data_ptr(), token if tokens > 1 else 0,
+                              head if heads > 1 else 0, dim))
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 tensor [sequences, pages of a sequence]")
     seqs, width = page_table.shape
     for t, n, what in ((cu, seqs + 1, "cu"), (starts, seqs, "starts")):
         if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous int32 tensor of shape {(n,)}")
-    tokens = k.shape[0]
-    tensors = []
-    for c, f, t, what in ((cache[0], fields[0], k, "keys"), (cache[2], fields[1], v, "values")):
-        token, head = _rows(t, (tokens, heads, c.shape[3]), k.dtype, what)
-        tensors.append(Tensor(*f, t.data_ptr(), token, head, c.shape[3]))
-    places = Places(page_table.data_ptr(), cu.data_ptr(), _i4._ptr(starts), seqs, width, tokens, heads, pages, size)
-    stream = _i4._stream(k, v, *cache)
+    stream = _i4._stream(rows[0], rows[1], kc, ks, vc, vs)
     _i4._stream(page_table, cu, starts)
-    _i4._done(fn, getattr(lib(), fn)(tensors[0], tensors[1], places, _i4._FLOATS[k.dtype], qt, stream))
+    places = Places(page_table.data_ptr(), cu.data_ptr(), _i4._ptr(starts), seqs, width, tokens, heads, pages, size)
+    _i4._done(fn, getattr(lib(), fn)(tensors[0], tensors[1], places, _i4._FLOATS[dt], qt, stream))
 
 
 def write(k, v, cache, page_table, cu, starts=None):
@@ -131,11 +126,10 @@ def write(k, v, cache, page_table, cu, starts=None):
     0).  Rows that belong to no sequence, and positions without a page (past the
     table, or a page number that is no page of the cache, as -1), are not
     written."""
-    described = _cache(cache)
     _i4._code(_i4._FLOATS, k.dtype, "keys")
     if k.dim() != 3:
         raise ValueError("keys must be a tensor [tokens, heads, dim]")
-    _call("kv8_write", cache, described, k, v, page_table, cu, starts)
+    _call("kv8_write", cache, (k, v), page_table, cu, starts)
 
 
 def read(cache, page_table, cu, starts=None, tokens=None, out_dtype=torch.bfloat16, out=None):
@@ -145,16 +139,18 @@ def read(cache, page_table, cu, starts=None, tokens=None, out_dtype=torch.bfloat
     Positions without a page give zeros.  out: the two tensors to write instead,
     whose rows that belong to no sequence are left as they are (new tensors'
     are unspecified)."""
-    described = _cache(cache)
     if out is None:
         if tokens is None:
             raise ValueError("read needs tokens, the number of rows, or out")
         _i4._code(_i4._FLOATS, out_dtype, "output")
         kc, _, vc, _ = cache
-        out = tuple(torch.empty(tokens, c.shape[2], c.shape[3], dtype=out_dtype, device=c.device) for c in (kc, vc))
+        if kc.dim() != 4 or vc.dim() != 4:
+            raise ValueError("a cache's codes are two tensors [pages, page_size, heads, dim]")
+        out = (torch.empty(tokens, kc.shape[2], kc.shape[3], dtype=out_dtype, device=kc.device),
+               torch.empty(tokens, vc.shape[2], vc.shape[3], dtype=out_dtype, device=vc.device))
     else:
         if out[0].dim() != 3 or (tokens is not None and out[0].shape[0] != tokens):
             raise ValueError("out must be two tensors [tokens, heads, dim]")
         _i4._code(_i4._FLOATS, out[0].dtype, "output")
-    _call("kv8_read", cache, described, out[0], out[1], page_table, cu, starts)
+    _call("kv8_read", cache, out, page_table, cu, starts)
     return out
