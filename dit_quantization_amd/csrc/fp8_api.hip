@@ -61,7 +61,7 @@ int fp8_quantize_act(const void* x, int64_t x_stride, const void* gate, int64_t 
   if (gate && (gate_stride < cols || !mul_ok(rows, gate_stride))) return NVFP4_ERR_SHAPE;
   if (cols > kMaxCols || (group != 32 && group != 64 && group != 128)) return NVFP4_ERR_UNSUPPORTED;
   if (empty) return NVFP4_OK;
-  if (!rows_ok(x, x_dtype, x_stride) || (gate && !rows_ok(gate, x_dtype, gate_stride)) || !aligned(codes, 8) ||
+  if (!rows_ok(x, x_dtype, x_stride) || (gate && !rows_ok(gate, x_dtype, gate_stride)) || !aligned(codes, 16) ||
       !aligned(scales, 4))
     return NVFP4_ERR_ALIGN;
   hipStream_t s;

@@ -75,8 +75,8 @@ hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t
   return hipSuccess;
 }
 
-// ---- activations.  A row is cut into slots of 8 columns, filled up to whole
-// groups, and slots go to threads in order, so that a group is 4, 8 or 16
+// ---- activations.  A row is cut into slots of 16 columns, filled up to whole
+// groups, and slots go to threads in order, so that a group is 2, 4 or 8
 // neighbouring lanes.
 
 // g / (1 + exp(-g)) to within 2^-45 of itself: exp(-g) = 2^n exp(r), |r| <= ln 2
@@ -99,46 +99,103 @@ __device__ __forceinline__ double silu64(float g) {
   return z * __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
 }
 
-template <bool BF, bool SILU>
-__global__ __launch_bounds__(256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, uint32_t per, double q) {
-  // at / slots, per = 2^32 / slots rounded down: the first quotient is exact or one short
-  const uint32_t at = blockIdx.x * 256 + threadIdx.x;
-  uint32_t row = __umulhi(at, per), i = at - row * slots;
-  if (i >= slots) {
-    ++row;
-    i -= slots;
+// The same of a bf16 gate from a table in LDS: of both signs and all magnitudes
+// from 2^-16 up to 2^8.
+constexpr uint32_t kTableFirst = (127 - 16) << 7, kTableSize = 24 << 7;
+__device__ __forceinline__ void fill_table(double* table) {
+  for (uint32_t i = threadIdx.x; i < 2 * kTableSize; i += blockDim.x) {
+    const uint32_t bits = i < kTableSize ? kTableFirst + i : 0x8000u + kTableFirst + (i - kTableSize);
+    table[i] = silu64(bf16_bits_to_f32(bits));
   }
-  const int64_t r = row;
-  const int c = 8 * (int)i;
-  const bool live = r < a.rows && c < a.cols;
-  Vec8<BF> x, g;
-  x.zero();
-  g.zero();
-  if (live) {
-    x.load(a.x, r * a.x_stride + c);
-    if (SILU) g.load(a.gate, r * a.gate_stride + c);
-  }
-  double y[8], top = 0.0;
+  __syncthreads();
+}
+
+// f over the L = 2, 4 or 8 lanes of a group.
+template <class T, class F>
+__device__ __forceinline__ T group_all(T v, int L, F f) {
+  v = f(v, dpp<kDppXor1>(v));
+  if (L >= 4) v = f(v, dpp<kDppXor2>(v));
+  if (L >= 8) v = f(v, dpp<kDppHalfMirror>(v));
+  return v;
+}
+
+// TABLE (bf16 gates): a grid of as many workgroups as fit at once, each with
+// its own table.  For 8 million values and more: filling it costs 2 us, an
+// exponential 24 of 47 vector instructions a value.
+template <bool BF, bool SILU, bool TABLE>
+__global__ __launch_bounds__(TABLE ? 512 : 256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, uint32_t per,
+                                                                              uint32_t all, double q, double inv_q) {
+  __shared__ double table[TABLE ? 2 * kTableSize : 1];
+  if (TABLE) fill_table(table);
+  const int L = a.group / 16;
+  // (rounds of whole workgroups, so that all lanes of a group are there)
+  for (uint32_t first = blockIdx.x * blockDim.x; first < all; first += gridDim.x * blockDim.x) {
+    // at / slots, per = 2^32 / slots rounded down: the first quotient is exact or one short
+    const uint32_t at = first + threadIdx.x;
+    uint32_t row = __umulhi(at, per), i = at - row * slots;
+    if (i >= slots) {
+      ++row;
+      i -= slots;
+    }
+    const int64_t r = row;
+    const int c = 16 * (int)i;
+    const bool live = r < a.rows && c < a.cols;
+    Vec8<BF> x[2], g[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = (double)x.at(j);
-    if (SILU) y[j] *= silu64(g.at(j));
-    top = fmax(top, fabs(y[j]));
-  }
-  const int L = a.group / 8;
-  top = lanes_all(top, L, [](double p, double t) { return p > t ? p : t; });
-  const float s = scale_for(top, q);
-  if (live) {
-    *reinterpret_cast<u32x2*>(reinterpret_cast<uint8_t*>(a.codes) + r * a.cols + c) = encode_quotients(y, s, a.e4m3);
-    if ((i & (L - 1)) == 0) a.scales[r * (int64_t)(slots / L) + i / L] = s;
+    for (int h = 0; h < 2; ++h) {
+      x[h].zero();
+      g[h].zero();
+      if (live) {
+        x[h].load(a.x, r * a.x_stride + c + 8 * h);
+        if (SILU) g[h].load(a.gate, r * a.gate_stride + c + 8 * h);
+      }
+    }
+    double y[16], top = 0.0;
+    bool outside = false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      y[j] = (double)x[j / 8].at(j % 8);
+      if (SILU && !TABLE) y[j] *= silu64(g[j / 8].at(j % 8));
+      if (TABLE) {
+        const uint32_t w = g[j / 8].a[0][j % 8 / 2], bits = j & 1 ? w >> 16 : w & 0xFFFFu;
+        const uint32_t entry = (bits & 0x7FFFu) - kTableFirst;
+        outside |= entry >= kTableSize;
+        y[j] *= table[min(entry, kTableSize - 1) + (bits >> 15) * kTableSize];
+      }
+    }
+    if (TABLE && live && outside) {  // a lane with a zero or a gate beyond the table's range
+#pragma unroll 1
+      for (int j = 0; j < 16; ++j) {
+        // (a loop, so that this path takes no registers: values are read again)
+        const float gate = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(a.gate)[r * a.gate_stride + c + j]);
+        const double v = silu64(gate) * (double)bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(a.x)[r * a.x_stride + c + j]);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = k == j ? v : y[k];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = fmax(top, fabs(y[j]));
+    top = group_all(top, L, [](double p, double t) { return p > t ? p : t; });
+    float s = (float)quotient(top, q, inv_q);
+    s = s == 0.0f ? 1.0f : s;
+    if (live) {
+      u32x2 code[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (SILU || a.e4m3) code[h] = encode_quotients(y + 8 * h, s, a.e4m3);
+        else code[h] = encode(x[h], s, false);
+      }
+      *reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(a.codes) + r * a.cols + c) = u32x4{code[0].x, code[0].y, code[1].x, code[1].y};
+      if ((i & (L - 1)) == 0) a.scales[r * (int64_t)(slots / L) + i / L] = s;
+    }
   }
 }
 
 hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
-  const int L = all.group / 8;
-  const uint32_t slots = (uint32_t)((all.cols + all.group - 1) / all.group * L);
-  const uint32_t per = (uint32_t)(((uint64_t)1 << 32) / slots);  // slots >= 4
-  // at most 2^31 threads a launch, whole rows
+  const int L = all.group / 16;
+  const uint32_t slots = (uint32_t)((all.cols + all.group - 1) / all.group * L);  // >= 2
+  const uint32_t per = (uint32_t)(((uint64_t)1 << 32) / slots);
+  // at most 2^31 slots a launch, whole rows
   const int64_t step = ((int64_t)1 << 31) / slots;
   for (int64_t r0 = 0; r0 < all.rows; r0 += step) {
     ActArgs a = all;
@@ -148,14 +205,16 @@ hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
     if (a.gate) a.gate = reinterpret_cast<const char*>(all.gate) + r0 * all.gate_stride * size;
     a.codes = reinterpret_cast<char*>(all.codes) + r0 * all.cols;
     a.scales = all.scales + r0 * (slots / L);
-    const dim3 grid((unsigned)((a.rows * slots + 255) / 256));
+    const uint32_t n = (uint32_t)(a.rows * slots);
     const double q = a.e4m3 ? 448.0 : 127.0;
-#define ACT_CASE(BF, SILU) \
-  hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU>), grid, dim3(256), 0, stream, a, slots, per, q)
-    if (a.gate && a.bf16) ACT_CASE(true, true);
-    else if (a.gate) ACT_CASE(false, true);
-    else if (a.bf16) ACT_CASE(true, false);
-    else ACT_CASE(false, false);
+#define ACT_CASE(BF, SILU, TABLE, GRID)                                                                        \
+  hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU, TABLE>), dim3(GRID), dim3(TABLE ? 512 : 256), 0, stream, a, \
+                     slots, per, n, q, 1.0 / q)
+    if (a.gate && a.bf16 && n >= (1u << 19)) ACT_CASE(true, true, true, 768);
+    else if (a.gate && a.bf16) ACT_CASE(true, true, false, (n + 255) / 256);
+    else if (a.gate) ACT_CASE(false, true, false, (n + 255) / 256);
+    else if (a.bf16) ACT_CASE(true, false, false, (n + 255) / 256);
+    else ACT_CASE(false, false, false, (n + 255) / 256);
 #undef ACT_CASE
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

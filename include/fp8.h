@@ -66,7 +66,7 @@ int fp8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int
  *   codes  [rows, cols] of q_dtype (INT4_I8 or INT4_E4M3), scales fp32 [rows,
  *          ceil(cols / group)], both contiguous
  * cols % 16 != 0, a stride < cols: NVFP4_ERR_SHAPE; cols > 2^24:
- * NVFP4_ERR_UNSUPPORTED. x, gate and their rows 16-byte aligned, codes 8,
+ * NVFP4_ERR_UNSUPPORTED. x, gate, their rows and codes 16-byte aligned,
  * scales 4. (A product x g / (1 + exp(-g)) beyond fp32's range whose scale
  * leaves it too is a caller error.)
  */
