@@ -64,37 +64,38 @@ __device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b, uint32_t per)
   return q + (a - q * b >= b ? 1 : 0);
 }
 
-// A row is one token and head; T lanes have it, V vectors of 8 elements each,
-// and U rows at a time.
-template <bool BF, int T, int V, int U>
+// A row is one token and head; T lanes have it, 16 elements each, and U rows at
+// a time.
+template <bool BF, int T, int U>
 __global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3,
                                                         int64_t first, int per_block, uint32_t per_head) {
   __shared__ Places places;
   const kv8_tensor& c = blockIdx.y ? values : keys;
   const int64_t t0 = first + (int64_t)blockIdx.x * per_block;
   const int n = locate_all(p, t0, per_block, places) * (int)p.heads;
-  const int lane = threadIdx.x % T;
+  const int lane = threadIdx.x % T, e = 16 * lane;
+  const double q = e4m3 ? 448.0 : 127.0, inv_q = e4m3 ? 1.0 / 448.0 : 1.0 / 127.0;
   for (int i0 = threadIdx.x / T; i0 < n; i0 += U * (256 / T)) {
-    Vec8<BF> v[U][V];
+    Vec8<BF> v[U][2];
     uint8_t* codes[U];
     float* scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * (256 / T);
       codes[u] = nullptr;
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[u][j].zero();
+      v[u][0].zero();
+      v[u][1].zero();
       if (i < n) {
         const int t = (int)divide((uint32_t)i, (uint32_t)p.heads, per_head), h = i - t * (int)p.heads;
         const Place at = places.at[t];
         if (at.page >= 0) {  // the same for the T lanes
           const int64_t row = (int64_t)at.row * p.heads + h;
-          codes[u] = reinterpret_cast<uint8_t*>(c.codes) + at.page * c.code_stride + row * c.dim;
+          codes[u] = reinterpret_cast<uint8_t*>(c.codes) + at.page * c.code_stride + row * c.dim + e;
           scale[u] = c.scales + at.page * c.scale_stride + row;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int e = 8 * (lane + T * j);
-            if (e < c.dim) v[u][j].load(c.rows, (t0 + t) * c.token_stride + h * c.head_stride + e);
+          if (e < c.dim) {
+            const int64_t from = (t0 + t) * c.token_stride + h * c.head_stride + e;
+            v[u][0].load(c.rows, from);
+            v[u][1].load(c.rows, from + 8);
           }
         }
       }
@@ -104,19 +105,20 @@ __global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_ten
       if (!codes[u]) continue;
       float top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(v[u][j].at(k)));
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(v[u][k / 8].at(k % 8)));
       const auto most = [](float a, float b) { return fmaxf(a, b); };
-      top = lanes_all<(T > 16 ? 16 : T)>(top, most);
-      if (T >= 32) top = most(top, __shfl_xor(top, 16));
-      if (T >= 64) top = most(top, __shfl_xor(top, 32));
-      const float s = scale_for((double)top, e4m3 ? 448.0 : 127.0);
+      if (T > 1) top = most(top, dpp<kDppXor1>(top));
+      if (T > 2) top = most(top, dpp<kDppXor2>(top));
+      if (T > 4) top = most(top, dpp<kDppHalfMirror>(top));
+      if (T > 8) top = most(top, dpp<kDppMirror>(top));
+      if (T > 16) top = most(top, __shfl_xor(top, 16));
+      if (T > 32) top = most(top, __shfl_xor(top, 32));
+      float s = (float)quotient((double)top, q, inv_q);
+      s = s == 0.0f ? 1.0f : s;
       if (lane == 0) *scale[u] = s;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = 8 * (lane + T * j);
-        if (e < c.dim) *reinterpret_cast<u32x2*>(codes[u] + e) = encode(v[u][j], s, e4m3);
+      if (e < c.dim) {
+        const u32x2 a = encode(v[u][0], s, e4m3), b = encode(v[u][1], s, e4m3);
+        *reinterpret_cast<u32x4*>(codes[u]) = u32x4{a.x, a.y, b.x, b.y};
       }
     }
   }
@@ -208,12 +210,17 @@ hipError_t launch_kv8(const kv8_tensor& keys, const kv8_tensor& values, const kv
 #undef READ_CASE
     });
   }
-#define WRITE_CASE(T, V)                                                                                          launch(p.heads * T, [&](dim3 g, int u, int64_t first, int n) {                                                    const auto kernel = bf16 ? u == 4 ? kv8_write_kernel<true, T, V, 4> : kv8_write_kernel<true, T, V, 1>                                    : u == 4 ? kv8_write_kernel<false, T, V, 4> : kv8_write_kernel<false, T, V, 1>;        hipLaunchKernelGGL(kernel, g, dim3(256), 0, stream, keys, values, p, e4m3, first, n, per_head);               })
-  if (dim <= 64) return WRITE_CASE(8, 1);
-  if (dim <= 128) return WRITE_CASE(16, 1);
-  if (dim <= 256) return WRITE_CASE(32, 1);
-  if (dim <= 512) return WRITE_CASE(64, 1);
-  return WRITE_CASE(64, 2);
+#define WRITE_CASE(T)                                                                                           \
+  launch(p.heads * T, [&](dim3 g, int u, int64_t first, int n) {                                                \
+    const auto kernel = bf16 ? u == 4 ? kv8_write_kernel<true, T, 4> : kv8_write_kernel<true, T, 1>             \
+                             : u == 4 ? kv8_write_kernel<false, T, 4> : kv8_write_kernel<false, T, 1>;          \
+    hipLaunchKernelGGL(kernel, g, dim3(256), 0, stream, keys, values, p, e4m3, first, n, per_head);             \
+  })
+  if (dim <= 64) return WRITE_CASE(4);
+  if (dim <= 128) return WRITE_CASE(8);
+  if (dim <= 256) return WRITE_CASE(16);
+  if (dim <= 512) return WRITE_CASE(32);
+  return WRITE_CASE(64);
 #undef WRITE_CASE
 }
 

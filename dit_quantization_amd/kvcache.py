@@ -17,6 +17,7 @@ run on torch's current stream.
     k, v = kvcache.read(cache, page_table, cu_all, tokens=total)      # bf16, everything the sequences hold
 """
 import ctypes
+import struct
 
 import torch
 
@@ -72,8 +73,6 @@ def new(pages, page_size, heads, dim, value_dim=None, dtype=torch.int8, device="
 
 def _page_stride(t, page, what):
     """Elements from page to page of a tensor of pages of `page` elements, which are contiguous."""
-    if t.is_contiguous():
-        return page
     inner = 1
     for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
         if size > 1 and stride != inner:
@@ -82,41 +81,62 @@ def _page_stride(t, page, what):
     return t.stride(0) if t.shape[0] > 1 else page
 
 
-def _call(fn, cache, rows, page_table, cu, starts):
+def _refuse_cache(cache):
+    got = ", ".join(f"{t.dtype} {tuple(t.shape)}" for t in cache)
+    raise ValueError("a cache is (codes, scales) of keys and of values: int8 or float8_e4m3fn codes [pages, page_size, "
+                     f"heads, dim] of one type that agree but for dim, float32 scales [pages, page_size, heads]; got {got}")
+
+
+def _rows(t, shape, dtype, c, s, places, what):
+    """The Tensor of a cache's tensor c with its scales s and of rows t [tokens, heads, dim]."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)}; got {t.dtype} {tuple(t.shape)}")
+    tokens, heads, dim = shape
+    token, head, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{what}'s heads must be contiguous")
+    page = places[1] * places[2]
+    return _TENSOR(_PACK(c.data_ptr(), s.data_ptr(),
+                         page * dim if c.is_contiguous() else _page_stride(c, page * dim, "codes"),
+                         page if s.is_contiguous() else _page_stride(s, page, "scales"), t.data_ptr(),
+                         token if tokens > 1 else 0, head if heads > 1 else 0, dim))
+
+
+# (What every call does is kept short, as in int4: a decode step's call costs
+# the host more than the GPU.)
+_PACK, _PACK_PLACES = struct.Struct("8q").pack, struct.Struct("9q").pack
+_TENSOR, _PLACES = Tensor.from_buffer_copy, Places.from_buffer_copy
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _call(fn, cache, k, v, page_table, cu, starts):
     """Checks a cache, rows of keys and values [tokens, heads, dim] and the tables, and calls fn."""
     kc, ks, vc, vs = cache
+    held, vheld = kc.shape, vc.shape
     qt = _i4._BYTES.get(kc.dtype)
-    if qt is None or kc.dim() != 4 or vc.dim() != 4 or vc.dtype != kc.dtype or kc.shape[:3] != vc.shape[:3]:
-        raise ValueError("a cache's codes are two int8 or float8_e4m3fn tensors [pages, page_size, heads, dim] that agree "
-                         f"but for dim; got {kc.dtype} {tuple(kc.shape)}, {vc.dtype} {tuple(vc.shape)}")
-    dt = rows[0].dtype
-    tokens = rows[0].shape[0]
-    pages, size, heads, _ = kc.shape
-    tensors = []
-    for c, s, t, what in ((kc, ks, rows[0], "keys"), (vc, vs, rows[1], "values")):
-        dim = c.shape[3]
-        if s.dtype != torch.float32 or s.shape != c.shape[:3]:
-            raise ValueError(f"a cache's scales are float32 tensors of shape {tuple(c.shape[:3])}; got {s.dtype} "
-                             f"{tuple(s.shape)}")
-        if t.shape != (tokens, heads, dim) or t.dtype != dt:
-            raise ValueError(f"{what} must be a {dt} tensor of shape {(tokens, heads, dim)}; got {t.dtype} "
-                             f"{tuple(t.shape)}")
-        token, head, one = t.stride()
-        if one != 1 and dim > 1:
-            raise ValueError(f"{what}'s heads must be contiguous")
-        tensors.append(Tensor(c.data_ptr(), s.data_ptr(), _page_stride(c, size * heads * dim, "codes"),
-                              _page_stride(s, size * heads, "scales"), t.data_ptr(), token if tokens > 1 else 0,
-                              head if heads > 1 else 0, dim))
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+    places = held[:3]
+    if (qt is None or len(held) != 4 or len(vheld) != 4 or vheld[:3] != places or vc.dtype != kc.dtype
+            or ks.shape != places or vs.shape != places or ks.dtype != _F32 or vs.dtype != _F32):
+        _refuse_cache(cache)
+    dtype, tokens = k.dtype, k.shape[0]
+    pages, size, heads = places
+    keys = _rows(k, (tokens, heads, held[3]), dtype, kc, ks, places, "keys")
+    values = _rows(v, (tokens, heads, vheld[3]), dtype, vc, vs, places, "values")
+    table = page_table.shape
+    if page_table.dtype != _I32 or len(table) != 2 or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 tensor [sequences, pages of a sequence]")
-    seqs, width = page_table.shape
-    for t, n, what in ((cu, seqs + 1, "cu"), (starts, seqs, "starts")):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
-            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {(n,)}")
-    stream = _i4._stream(rows[0], rows[1], kc, ks, vc, vs)
+    seqs, width = table
+    if cu.dtype != _I32 or cu.shape != (seqs + 1,) or not cu.is_contiguous():
+        raise ValueError(f"cu must be a contiguous int32 tensor of shape {(seqs + 1,)}")
+    first = None
+    if starts is not None:
+        if starts.dtype != _I32 or starts.shape != (seqs,) or not starts.is_contiguous():
+            raise ValueError(f"starts must be a contiguous int32 tensor of shape {(seqs,)}")
+        first = starts.data_ptr()
+    stream = _i4._stream(k, v, kc, ks, vc, vs)
     _i4._stream(page_table, cu, starts)
-    places = Places(page_table.data_ptr(), cu.data_ptr(), _i4._ptr(starts), seqs, width, tokens, heads, pages, size)
-    _i4._done(fn, getattr(lib(), fn)(tensors[0], tensors[1], places, _i4._FLOATS[dt], qt, stream))
+    at = _PLACES(_PACK_PLACES(page_table.data_ptr(), cu.data_ptr(), first or 0, seqs, width, tokens, heads, pages, size))
+    _i4._done(fn, getattr(_lib or lib(), fn)(keys, values, at, _i4._FLOATS[dtype], qt, stream))
 
 
 def write(k, v, cache, page_table, cu, starts=None):
@@ -129,7 +149,7 @@ def write(k, v, cache, page_table, cu, starts=None):
     _i4._code(_i4._FLOATS, k.dtype, "keys")
     if k.dim() != 3:
         raise ValueError("keys must be a tensor [tokens, heads, dim]")
-    _call("kv8_write", cache, (k, v), page_table, cu, starts)
+    _call("kv8_write", cache, k, v, page_table, cu, starts)
 
 
 def read(cache, page_table, cu, starts=None, tokens=None, out_dtype=torch.bfloat16, out=None):
@@ -143,14 +163,15 @@ def read(cache, page_table, cu, starts=None, tokens=None, out_dtype=torch.bfloat
         if tokens is None:
             raise ValueError("read needs tokens, the number of rows, or out")
         _i4._code(_i4._FLOATS, out_dtype, "output")
-        kc, _, vc, _ = cache
-        if kc.dim() != 4 or vc.dim() != 4:
-            raise ValueError("a cache's codes are two tensors [pages, page_size, heads, dim]")
-        out = (torch.empty(tokens, kc.shape[2], kc.shape[3], dtype=out_dtype, device=kc.device),
-               torch.empty(tokens, vc.shape[2], vc.shape[3], dtype=out_dtype, device=vc.device))
+        held, vheld = cache[0].shape, cache[2].shape
+        if len(held) != 4 or len(vheld) != 4:
+            _refuse_cache(cache)
+        device = cache[0].device
+        out = (torch.empty(tokens, held[2], held[3], dtype=out_dtype, device=device),
+               torch.empty(tokens, vheld[2], vheld[3], dtype=out_dtype, device=device))
     else:
         if out[0].dim() != 3 or (tokens is not None and out[0].shape[0] != tokens):
             raise ValueError("out must be two tensors [tokens, heads, dim]")
         _i4._code(_i4._FLOATS, out[0].dtype, "output")
-    _call("kv8_read", cache, out, page_table, cu, starts)
+    _call("kv8_read", cache, *out, page_table, cu, starts)
     return out
