@@ -2,6 +2,7 @@
 //   y[m, n] = sum_b xs[m, b] ws[n / 128, b] sum_{k in b} x[m, k] w[n, k]
 // with b the blocks of 128 columns.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -234,111 +235,248 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
 // the matrix instruction and are added to the running ones by a multiply-add,
 // which the vector units do while the matrix unit has the next tiles.
 // WIDE: widened to bf16 on the way to the matrix instruction (fp32 outputs).
+
+// A workgroup's tile and where its operands lie.
+template <int BM, int BN, int WM, int WN>
+struct TileOf {
+  static constexpr int NT = WM * WN * 64, NW = WM * WN;
+  static constexpr int WBM = BM / WM, WBN = BN / WN;        // a wave's tile
+  static constexpr int TM = WBM / 16, TN = WBN / 16;
+  static constexpr int XD = BM * 8 / NT, WD = BN * 8 / NT;  // 16-byte loads a lane and block
+  static constexpr int XSW = (BM + 63) / 64;                // waves that load x's scales
+  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && XSW < NW && TM >= 2, "tile and waves");
+  static_assert(128 % WBN == 0, "a wave's rows of the weight share a scale");
+
+  int lane, wave, wm, wn, l16, g, n0, rows, wrows, G;
+  int64_t m0;
+  __amdgpu_buffer_rsrc_t xbuf, wbuf, scbuf;
+  uint32_t sc_off;
+
+  __device__ __forceinline__ explicit TileOf(const Fp8Product& p) {
+    const int tid = threadIdx.x;
+    lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    wm = wave / WN;
+    wn = wave % WN;
+    l16 = lane & 15;
+    g = lane >> 4;
+    // tiles in groups of p.group tiles of x, so that an XCD's share rows of both operands in its L2
+    const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (int)((p.M + BM - 1) / BM);
+    const int bid = xcd_run((int)blockIdx.x, tiles_m * tiles_n);
+    const int first = bid / (p.group * tiles_n) * p.group, gsize = min(tiles_m - first, p.group);
+    const int in = bid % (p.group * tiles_n);
+    m0 = (int64_t)(first + in % gsize) * BM;
+    n0 = in / gsize * BN;
+    rows = (int)min((int64_t)BM, p.M - m0);
+    wrows = min(BN, p.N - n0);
+    G = (p.K + 127) / 128;
+    xbuf = make_buf(p.x + m0 * p.K, (uint32_t)rows * (uint32_t)p.K);
+    wbuf = make_buf(p.w + (int64_t)n0 * p.K, (uint32_t)wrows * (uint32_t)p.K);
+    // The first waves load x's scales (a row past the end takes the last one's: a
+    // normal number), the next one those of the weight.
+    const __amdgpu_buffer_rsrc_t sbuf = make_buf(p.xs + m0 * G, (uint32_t)rows * (uint32_t)G * 4u);
+    const __amdgpu_buffer_rsrc_t wsbuf =
+        make_buf(p.ws + (int64_t)(n0 / 128) * G, (uint32_t)((wrows + 127) / 128) * (uint32_t)G * 4u);
+    scbuf = wave < XSW ? sbuf : wsbuf;
+    sc_off = (uint32_t)(wave < XSW ? min(tid, rows - 1) : lane) * (uint32_t)G * 4u;
+  }
+
+  // A load has 8 rows, the first a multiple of 8: lane l row l / 8, into slot l %
+  // 8 the chunk (l % 8) ^ (row / 2 % 8), so that the fragment reads of 16 rows
+  // meet all banks.  Byte offset of the chunk in the block, and of the load.
+  __device__ __forceinline__ uint32_t chunk_at(int row) const {
+    return (16u * (uint32_t)((lane & 7) ^ (lane >> 4))) ^ (uint32_t)((row & 8) << 3);
+  }
+  __device__ __forceinline__ uint32_t load_at(int row, int K) const {
+    return (uint32_t)(row + (lane >> 3)) * (uint32_t)K + chunk_at(row);
+  }
+  // x's loads of a block: chunks past a row's end are zeros.  (The weight's are
+  // whatever its next row holds, or zeros behind the last.)
+  __device__ __forceinline__ void load_x(u32x4* to, int row, uint32_t off, uint32_t k, int K) const {
+    buffer_to_lds16(xbuf, to + 8 * row, k + chunk_at(row) < (uint32_t)K ? off : kBufOOB, k);
+  }
+  // The scales of the 4 blocks from b on, a row 16 bytes (past a row's end
+  // whatever the next one holds), every fourth time; in between, and in the
+  // waves behind, the load fetches nothing and goes nowhere (no branches: they
+  // would split the step).
+  __device__ __forceinline__ void load_scales(f32x4* to, f32x4* unused, int b, uint32_t k) const {
+    const bool due = ((b & 3) == 0) & (b < G) & (wave <= XSW);
+    buffer_to_lds16(scbuf, reinterpret_cast<u32x4*>(due ? to + 64 * wave : unused), due ? sc_off : kBufOOB, k / 32);
+  }
+  // Factors xs ws of block b for the lane's rows of x, from LDS.
+  __device__ __forceinline__ void read_scales(const f32x4* from, int b, float (&x)[TM], float& w) const {
+    const float* of = reinterpret_cast<const float*>(from) + (b & 3);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) x[j] = of[4 * (wm * WBM + 16 * j + l16)];
+    w = of[4 * (64 * XSW + wn * WBN / 128)];
+  }
+  // Those that are no normal number count as 0 (see other_blocks).
+  static __device__ __forceinline__ void factors(const float (&x)[TM], float w, float (&s)[TM], bool& odd) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const float v = x[j] * w;
+      const bool o = not_normal(v);
+      s[j] = o ? 0.0f : v;
+      odd |= o;
+    }
+  }
+
+  // Products of scales that are no normal number could leave fp32's range
+  // although xs ws d does not: their blocks are taken again, straight from memory.
+  template <bool WIDE>
+  __device__ __forceinline__ void other_blocks(const Fp8Product& p, f32x4 (&acc)[TN][TM]) const {
+#pragma unroll 1
+    for (int b = 0; b < G; ++b) {
+      const float wsc = p.ws[(int64_t)(min(n0 + wn * WBN, p.N - 1) / 128) * G + b];
+      double f[TM];
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const float v = p.xs[(m0 + min(wm * WBM + 16 * j + l16, rows - 1)) * G + b];
+        const bool o = not_normal(v * wsc);
+        f[j] = o ? (double)v * (double)wsc : 0.0;
+        any |= o;
+      }
+      if (!__ballot(any)) continue;
+      const auto fragment = [&](__amdgpu_buffer_rsrc_t buf, int r, Fragment8<WIDE>& v) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k = 128u * (uint32_t)b + 64u * h + 16u * (uint32_t)g;
+          v.q[h] = __builtin_amdgcn_raw_buffer_load_b128(
+              buf, k < (uint32_t)p.K ? (uint32_t)r * (uint32_t)p.K + k : kBufOOB, 0, 0);
+        }
+      };
+      Fragment8<WIDE> x[TM], w;
+#pragma unroll
+      for (int j = 0; j < TM; ++j) fragment(xbuf, wm * WBM + 16 * j + l16, x[j]);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        fragment(wbuf, wn * WBN + 16 * i + l16, w);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const f32x4 e = w.times(x[j]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += (float)((double)e[r] * f[j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  template <int LDS>
+  __device__ __forceinline__ void store(const Fp8Product& p, void* lds, const f32x4 (&acc)[TN][TM]) const {
+    // A lane has, of a tile, one row of x and four rows of the weight.  bf16
+    // rows go through LDS (a wave's own part of the stages, 16-byte chunks
+    // swizzled by the row) and out as 16 bytes a lane, non-temporal: y is not
+    // read again here.
+    constexpr int RC = WBN / 8;  // 16-byte chunks of a wave's bf16 rows
+    const int nw = n0 + wn * WBN;
+    if (p.bf16 && (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
+      static_assert(WBM * WBN * 2 * NW <= LDS && WBM * RC % 64 == 0, "the tile fits the stages");
+      __builtin_amdgcn_s_barrier();  // every wave has read the stages (its reads are waited for above)
+      uint32_t* out = reinterpret_cast<uint32_t*>(lds) + wave * (WBM * WBN / 2);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int m = 16 * j + l16;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const f32x4 v = acc[i][j];
+          *reinterpret_cast<u32x2*>(out + (m * RC + ((2 * i + (g >> 1)) ^ (l16 & (RC - 1)))) * 4 + 2 * (g & 1)) =
+              u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+      __builtin_amdgcn_wave_barrier();
+      uint16_t* y = reinterpret_cast<uint16_t*>(p.y);
+#pragma unroll
+      for (int q = 0; q < WBM * RC / 64; ++q) {
+        const int m = (64 * q + lane) / RC, c = lane & (RC - 1);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(out + (m * RC + (c ^ (m & 15 & (RC - 1)))) * 4);
+        const int row = wm * WBM + m, n = nw + 8 * c;
+        if (row < rows && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (m0 + row) * p.N + n));
+      }
+      return;
+    }
+    const bool fours = !p.bf16 && (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int m = wm * WBM + 16 * j + l16;
+      if (m >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const int n = nw + 16 * i + 4 * g;
+        const int64_t at = (m0 + m) * p.N + n;
+        if (fours) {
+          if (n < p.N) __builtin_nontemporal_store(acc[i][j], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at));
+          continue;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (n + r >= p.N) break;
+          if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at + r] = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
+          else reinterpret_cast<float*>(p.y)[at + r] = acc[i][j][r];
+        }
+      }
+    }
+  }
+};
+
+// Large tiles: registers for one block's fragments of x and four of the weight's
+// only, so a step meets twice, once for each half of what the loads overwrite.
+// 4096 x 14336 x 4096 to bf16: 225 us, 2.14 PFLOP/s (256 x 256, 8 waves); it
+// waits for the fill of the L2s and, with the clock at its power limit, for the matrix
+// units.
 template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
 __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_tile_kernel(Fp8Product p) {
-  constexpr int NT = WM * WN * 64, NW = WM * WN;
-  constexpr int WBM = BM / WM, WBN = BN / WN;        // a wave's tile
-  constexpr int TM = WBM / 16, TN = WBN / 16;
-  constexpr int XD = BM * 8 / NT, WD = BN * 8 / NT;  // 16-byte loads a lane and step
-  constexpr int XSW = (BM + 63) / 64;                // waves that load x's scales
+  using Tile = TileOf<BM, BN, WM, WN>;
+  constexpr int XD = Tile::XD, WD = Tile::WD, TM = Tile::TM, TN = Tile::TN, WBM = Tile::WBM, WBN = Tile::WBN;
   constexpr int LAST = 2, WB = 4;                    // rows of tiles behind a step's second barrier; fragments held
-  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0 && WD % 2 == 0 && XSW < NW && TN % 4 == 0, "tile and waves");
-  static_assert(128 % WBN == 0, "a wave's rows of the weight share a scale");
   struct Stages {
     u32x4 x[NS][BM * 8], w[NS][BN * 8];
-    f32x4 scales[2][(XSW + 1) * 64], unused[64];  // of 4 blocks a row
+    f32x4 scales[2][(Tile::XSW + 1) * 64], unused[64];  // of 4 blocks a row
   };
   __shared__ __attribute__((aligned(16))) Stages st;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const int l16 = lane & 15, g = lane >> 4;
-  const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (int)((p.M + BM - 1) / BM);
-  // tiles in groups of 4 tiles of x, so that an XCD's tiles share rows of both operands in its L2
-  constexpr int GROUP = 4;
-  const int bid = xcd_run((int)blockIdx.x, tiles_m * tiles_n);
-  const int first = bid / (GROUP * tiles_n) * GROUP, gsize = min(tiles_m - first, GROUP);
-  const int in = bid % (GROUP * tiles_n);
-  const int64_t m0 = (int64_t)(first + in % gsize) * BM;
-  const int n0 = in / gsize * BN;
-  const int rows = (int)min((int64_t)BM, p.M - m0), wrows = min(BN, p.N - n0);
-  const int G = (p.K + 127) / 128;
+  const Tile t(p);
+  const int wave = t.wave, G = t.G;
 
-  // Loads of 8 rows: lane l has row l / 8 and stores to slot l % 8 its chunk
-  // (l % 8) ^ (row / 2 % 8); the 8 rows start at a multiple of 8.  A wave's
-  // loads of the weight are half of the first halves of the WN waves' rows,
-  // half of the second halves.
-  const __amdgpu_buffer_rsrc_t xbuf = make_buf(p.x + m0 * p.K, (uint32_t)rows * (uint32_t)p.K);
-  const __amdgpu_buffer_rsrc_t wbuf = make_buf(p.w + (int64_t)n0 * p.K, (uint32_t)wrows * (uint32_t)p.K);
+  // A wave's loads of the weight are half of the first halves of the WN waves'
+  // rows, half of the second halves (and x's go by the same order where there
+  // are as many: fewer offsets).
   const auto w_at = [&](int j) {
-    const int t = 8 * (wave * (WD / 2) + j % (WD / 2)), half = j / (WD / 2);
-    return t / (WBN / 2) * WBN + half * (WBN / 2) + t % (WBN / 2);
+    const int r = 8 * (wave * (WD / 2) + j % (WD / 2)), half = j / (WD / 2);
+    return r / (WBN / 2) * WBN + half * (WBN / 2) + r % (WBN / 2);
   };
-  // (x's rows go by the same order where there are as many: fewer offsets)
   const auto x_at = [&](int j) { return XD == WD ? w_at(j) : 8 * (wave * XD + j); };
-  const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));
-  const auto chunk_at = [&](int row) { return chunk ^ (uint32_t)((row & 8) << 3); };
   uint32_t x_off[XD], w_off[WD];
 #pragma unroll
-  for (int j = 0; j < XD; ++j) x_off[j] = (uint32_t)(x_at(j) + (lane >> 3)) * (uint32_t)p.K + chunk_at(x_at(j));
+  for (int j = 0; j < XD; ++j) x_off[j] = t.load_at(x_at(j), p.K);
 #pragma unroll
-  for (int j = 0; j < WD; ++j) w_off[j] = (uint32_t)(w_at(j) + (lane >> 3)) * (uint32_t)p.K + chunk_at(w_at(j));
-  // The first waves load x's scales (a row past the end takes the last one's: a
-  // normal number), the next one those of the weight.
-  const __amdgpu_buffer_rsrc_t sbuf = make_buf(p.xs + m0 * G, (uint32_t)rows * (uint32_t)G * 4u);
-  const __amdgpu_buffer_rsrc_t wsbuf =
-      make_buf(p.ws + (int64_t)(n0 / 128) * G, (uint32_t)((wrows + 127) / 128) * (uint32_t)G * 4u);
-  const __amdgpu_buffer_rsrc_t scbuf = wave < XSW ? sbuf : wsbuf;
-  const uint32_t sc_off = (uint32_t)(wave < XSW ? min(tid, rows - 1) : lane) * (uint32_t)G * 4u;
+  for (int j = 0; j < WD; ++j) w_off[j] = t.load_at(w_at(j), p.K);
   // Load q of block b (the last one again past the end): 0 .. XD - 1 x, then
   // the first and the second half of the weight's.
   constexpr int L1 = XD + WD / 2, L2 = WD / 2;
-  const auto dma = [&](int stage, int blk, int q) {
-    const int b = min(blk, G - 1);
-    const uint32_t k = 128u * (uint32_t)b;
-    if (q < XD) {
-      // chunks past a row's end: zeros for x, and whatever the next row of the
-      // weight holds (zeros behind the last) for the weight
-      buffer_to_lds16(xbuf, st.x[stage] + 8 * x_at(q), k + chunk_at(x_at(q)) < (uint32_t)p.K ? x_off[q] : kBufOOB, k);
-    } else {
-      buffer_to_lds16(wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
-    }
+  const auto dma = [&](int stage, int b, int q) {
+    const uint32_t k = 128u * (uint32_t)min(b, G - 1);
+    if (q < XD) t.load_x(st.x[stage], x_at(q), x_off[q], k, p.K);
+    else buffer_to_lds16(t.wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
   };
-  // The scales of the 4 blocks from b on, a row 16 bytes (past a row's end
-  // whatever the next one holds), every fourth time; in between, and in the
-  // waves behind, the load fetches nothing and goes nowhere.
   static_assert(NS <= 5, "a block's scales are read before those of the block 8 later come");
   const auto dma_scales = [&](int b) {
-    const bool due = ((b & 3) == 0) & (b < G) & (wave <= XSW);  // (no branches: they would split the step)
-    buffer_to_lds16(scbuf, reinterpret_cast<u32x4*>(due ? st.scales[(b >> 2) & 1] + 64 * wave : st.unused),
-                    due ? sc_off : kBufOOB, 4u * (uint32_t)min(b, G - 1));
+    t.load_scales(st.scales[(b >> 2) & 1], st.unused, b, 128u * (uint32_t)min(b, G - 1));
   };
 
   // Fragments: chunks g and g + 4 of a row, the same columns of both operands.
-  const int sw = (l16 >> 1) & 7;
-  const int x_row = (wm * WBM + l16) * 8, w_row = (wn * WBN + l16) * 8;
-  const int x0 = x_row + (g ^ sw), x1 = x_row + ((g + 4) ^ sw), w0 = w_row + (g ^ sw), w1 = w_row + ((g + 4) ^ sw);
+  const int c0 = t.g ^ ((t.l16 >> 1) & 7), c1 = c0 ^ 4;
+  const int x_row = (t.wm * WBM + t.l16) * 8, w_row = (t.wn * WBN + t.l16) * 8;
+  const int x0 = x_row + c0, x1 = x_row + c1, w0 = w_row + c0, w1 = w_row + c1;
   Fragment8<WIDE> xf[TM], wf[WB];
   float s[TM], xsc[TM], wsc, s_last = 0.0f;
   bool odd = false;
   const auto load_x = [&](int stage, int j, int h) { xf[j].q[h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
   const auto load_w = [&](int stage, int i, int h) { wf[i % WB].q[h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
-  const auto load_scales = [&](int b) {
-    const float* of = reinterpret_cast<const float*>(st.scales[(b >> 2) & 1]) + (b & 3);
-#pragma unroll
-    for (int j = 0; j < TM; ++j) xsc[j] = of[4 * (wm * WBM + 16 * j + l16)];
-    wsc = of[4 * (64 * XSW + wn * WBN / 128)];
-  };
-  // factors of a block; those that are no normal number count as 0 here
-  const auto factors = [&] {
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const float v = xsc[j] * wsc;
-      const bool o = not_normal(v);
-      s[j] = o ? 0.0f : v;
-      odd |= o;
-    }
-  };
+  const auto load_scales = [&](int b) { t.read_scales(st.scales[(b >> 2) & 1], b, xsc, wsc); };
+  const auto factors = [&] { Tile::factors(xsc, wsc, s, odd); };
 
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -455,99 +593,145 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   for (int q = TILES - LAG; q < TILES; ++q) add(q, s_last);
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
 
-  // Products of scales that are no normal number could leave fp32's range
-  // although xs ws d does not: they counted as 0 above, and their blocks are
-  // taken again, straight from memory.
-  if (__ballot(odd)) {
-#pragma unroll 1
-    for (b = 0; b < G; ++b) {
-      const float wsc = p.ws[(int64_t)(min(n0 + wn * WBN, p.N - 1) / 128) * G + b];
-      double f[TM];
-      bool any = false;
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        const float v = p.xs[(m0 + min(wm * WBM + 16 * j + l16, rows - 1)) * G + b];
-        const bool o = not_normal(v * wsc);
-        f[j] = o ? (double)v * (double)wsc : 0.0;
-        any |= o;
-      }
-      if (!__ballot(any)) continue;
-      const auto fragment = [&](__amdgpu_buffer_rsrc_t buf, int r, u32x4 (&q)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t k = 128u * (uint32_t)b + 64u * h + 16u * (uint32_t)g;
-          q[h] = __builtin_amdgcn_raw_buffer_load_b128(buf, k < (uint32_t)p.K ? (uint32_t)r * (uint32_t)p.K + k : kBufOOB, 0, 0);
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < TM; ++j) fragment(xbuf, wm * WBM + 16 * j + l16, xf[j].q);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        fragment(wbuf, wn * WBN + 16 * i + l16, wf[i % WB].q);
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          const f32x4 e = multiply(i, j);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] += (float)((double)e[r] * f[j]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-  }
+  if (__ballot(odd)) t.template other_blocks<WIDE>(p, acc);
+  t.template store<(int)sizeof(st)>(p, &st, acc);
+}
 
-  // A lane has, of a tile, one row of x and four rows of the weight.  bf16
-  // rows go through LDS (a wave's own part of the stages, 16-byte chunks
-  // swizzled by the row) and out as 16 bytes a lane, non-temporal: y is not
-  // read again here.
-  constexpr int RC = WBN / 8;  // 16-byte chunks of a wave's bf16 rows
-  const int nw = n0 + wn * WBN;
-  if (!WIDE && (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
-    static_assert(WBM * WBN * 2 * NW <= (int)sizeof(st) && WBM * RC % 64 == 0, "the tile fits the stages");
-    __builtin_amdgcn_s_barrier();  // every wave has read the stages (its reads are waited for above)
-    uint32_t* out = reinterpret_cast<uint32_t*>(&st) + wave * (WBM * WBN / 2);
+// Small tiles: the fragments of two blocks fit the registers, so the next
+// block's are read while this one's are multiplied, and a step meets once.
+// 333 x 5000 x 4112 with 64 x 128 tiles, the kernel above and this one: 27.2 and
+// 22.9 us to bf16, 33.7 and 26.8 to fp32.
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_pipe_kernel(Fp8Product p) {
+  using Tile = TileOf<BM, BN, WM, WN>;
+  constexpr int XD = Tile::XD, WD = Tile::WD, TM = Tile::TM, TN = Tile::TN, WBM = Tile::WBM, WBN = Tile::WBN;
+  struct Stages {
+    u32x4 x[NS][BM * 8], w[NS][BN * 8];
+    f32x4 scales[2][(Tile::XSW + 1) * 64], unused[64];  // of 4 blocks a row
+  };
+  __shared__ __attribute__((aligned(16))) Stages st;
+
+  const Tile t(p);
+  const int wave = t.wave, G = t.G;
+
+  const auto x_at = [&](int j) { return 8 * (wave * XD + j); };
+  const auto w_at = [&](int j) { return 8 * (wave * WD + j); };
+  uint32_t x_off[XD], w_off[WD];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int m = 16 * j + l16;
+  for (int j = 0; j < XD; ++j) x_off[j] = t.load_at(x_at(j), p.K);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        const f32x4 v = acc[i][j];
-        *reinterpret_cast<u32x2*>(out + (m * RC + ((2 * i + (g >> 1)) ^ (l16 & (RC - 1)))) * 4 + 2 * (g & 1)) =
-            u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-      }
+  for (int j = 0; j < WD; ++j) w_off[j] = t.load_at(w_at(j), p.K);
+  // Load q of block b (the last one again past the end): x, then the weight, then the scales.
+  constexpr int LOADS = XD + WD + 1;
+  static_assert((NS - 1) * LOADS <= 63, "the counter of loads in flight");
+  static_assert(NS <= 5, "a block's scales are read before those of the block 8 later come");
+  const auto dma = [&](int stage, int b, int q) {
+    const uint32_t k = 128u * (uint32_t)min(b, G - 1);
+    if (q < XD) t.load_x(st.x[stage], x_at(q), x_off[q], k, p.K);
+    else if (q < XD + WD) buffer_to_lds16(t.wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
+    else t.load_scales(st.scales[(b >> 2) & 1], st.unused, b, k);
+  };
+
+  // Fragments: chunks g and g + 4 of a row, the same columns of both operands.
+  const int c0 = t.g ^ ((t.l16 >> 1) & 7), c1 = c0 ^ 4;
+  const int x_row = (t.wm * WBM + t.l16) * 8, w_row = (t.wn * WBN + t.l16) * 8;
+  const int x0 = x_row + c0, x1 = x_row + c1, w0 = w_row + c0, w1 = w_row + c1;
+  // Fragments of the block at hand and of the next.
+  Fragment8<WIDE> xf[2][TM], wf[2][TN];
+  float s[TM], xsc[2][TM], wsc[2], s_last = 0.0f, s_last2 = 0.0f;
+  bool odd = false;
+  // read r of a block: the fragments' halves in the order in which the tiles want them, W_0, X_0 .., W_1 ..
+  constexpr int READS = 2 * (TM + TN);
+  const auto read = [&](int set, int stage, int r) {
+    const int f = r / 2, h = r % 2;
+    if (f == 0 || f > TM) {
+      const int i = f == 0 ? 0 : f - TM;
+      wf[set][i].q[h] = st.w[stage][(h ? w1 : w0) + 128 * i];
+    } else {
+      xf[set][f - 1].q[h] = st.x[stage][(h ? x1 : x0) + 128 * (f - 1)];
     }
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    __builtin_amdgcn_wave_barrier();
-    uint16_t* y = reinterpret_cast<uint16_t*>(p.y);
+  };
+  const auto load_scales = [&](int set, int b) { t.read_scales(st.scales[(b >> 2) & 1], b, xsc[set], wsc[set]); };
+
+  f32x4 acc[TN][TM];
 #pragma unroll
-    for (int q = 0; q < WBM * RC / 64; ++q) {
-      const int m = (64 * q + lane) / RC, c = lane & (RC - 1);
-      const u32x4 v = *reinterpret_cast<const u32x4*>(out + (m * RC + (c ^ (m & 15 & (RC - 1)))) * 4);
-      const int row = wm * WBM + m, n = nw + 8 * c;
-      if (row < rows && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (m0 + row) * p.N + n));
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  // Tile q of a step, row of tiles after row.  A tile's sums are added two tiles
+  // later, while the matrix unit has the next ones (the first two of a step
+  // add the last two of the step before).
+  constexpr int TILES = TN * TM, LAG = 2;
+  static_assert(TILES % 4 == 0 && TM >= LAG, "d's entries follow the tiles; the last two are of different rows of x");
+  f32x4 d[4] = {};
+  const auto add = [&](int q, float f) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[q / TM][q % TM][r] = __builtin_fmaf(d[q % 4][r], f, acc[q / TM][q % TM][r]);
+  };
+  // Step b: its fragments are in registers (set b % 2; their reads were issued
+  // in the step before), so that once all waves are here its stage is free for
+  // block b + NS, whose loads have NS - 1 steps to land, and block b + 1 has
+  // landed for all.  The reads of block b + 1 and the loads go out between the
+  // tiles.
+  const auto step = [&](int b, int set, int& stage) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 2) * LOADS));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const int free = stage;
+    stage = stage + 1 == NS ? 0 : stage + 1;
+    s_last = s[TM - 1];
+    s_last2 = s[TM - 2];
+    Tile::factors(xsc[set], wsc[set], s, odd);
+    load_scales(set ^ 1, b + 1);
+#pragma unroll
+    for (int q = 0; q < TILES; ++q) {
+      constexpr int RT = (READS + TILES - 1) / TILES, LT = (LOADS + TILES - 1) / TILES;
+#pragma unroll
+      for (int r = RT * q; r < RT * (q + 1) && r < READS; ++r) read(set ^ 1, stage, r);
+#pragma unroll
+      for (int l = LT * q; l < LT * (q + 1) && l < LOADS; ++l) dma(free, b + NS, l);
+      d[q % 4] = wf[set][q / TM].times(xf[set][q % TM]);
+      if (q >= LAG) add(q - LAG, s[(q - LAG) % TM]);
+      else add(TILES + q - LAG, q == LAG - 1 ? s_last : s_last2);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    return;
+  };
+
+#pragma unroll
+  for (int b = 0; b < NS; ++b)
+#pragma unroll
+    for (int l = 0; l < LOADS; ++l) dma(b, b, l);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0((NS - 1) * LOADS));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  load_scales(0, 0);
+#pragma unroll
+  for (int r = 0; r < READS; ++r) read(0, 0, r);
+#pragma unroll
+  for (int j = 0; j < TM; ++j) s[j] = 0.0f;
+  int b = 0, stage = 0;
+  for (; b + 2 <= G; b += 2) {
+    step(b, 0, stage);
+    step(b + 1, 1, stage);
   }
-  const bool fours = !p.bf16 && (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+  if (b < G) step(b, 0, stage);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int m = wm * WBM + 16 * j + l16;
-    if (m >= rows) continue;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int n = nw + 16 * i + 4 * g;
-      const int64_t at = (m0 + m) * p.N + n;
-      if (fours) {
-        if (n < p.N) __builtin_nontemporal_store(acc[i][j], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at));
-        continue;
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (n + r >= p.N) break;
-        if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at + r] = (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
-        else reinterpret_cast<float*>(p.y)[at + r] = acc[i][j][r];
-      }
-    }
-  }
+  for (int q = TILES - LAG; q < TILES; ++q) add(q, s[q % TM]);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
+
+  if (__ballot(odd)) t.template other_blocks<WIDE>(p, acc);
+  t.template store<(int)sizeof(st)>(p, &st, acc);
+}
+
+// An XCD's workgroups run a contiguous stretch of tiles at a time, about 32 (one
+// a CU); what they fetch into its L2 is least where that is about as many rows
+// of x as of the weight: tiles of x a group.
+inline int group_of(int64_t tiles_m, int64_t tiles_n, int bm, int bn) {
+  const double at_once = std::min<double>(32.0, std::max<double>(1.0, (double)(tiles_m * tiles_n) / 8.0));
+  const double want = std::max(1.0, std::sqrt(at_once * bn / bm));  // tiles of x
+  const int64_t groups = std::max<int64_t>(1, (int64_t)((double)tiles_m / want + 0.5));
+  return (int)std::min<int64_t>((tiles_m + groups - 1) / groups, 64);
 }
 
 // Launches of a kernel with tiles of bm rows of x and bn of the weight: as many
@@ -562,6 +746,7 @@ hipError_t launch_tiles(const Fp8Product& all, int bm, int bn, F launch) {
     p.x += m0 * all.K;
     p.xs += m0 * ((all.K + 127) / 128);
     p.y = reinterpret_cast<char*>(all.y) + m0 * all.N * (all.bf16 ? 2 : 4);
+    p.group = group_of((p.M + bm - 1) / bm, tiles_n, bm, bn);
     launch(p, dim3((unsigned)((p.M + bm - 1) / bm * tiles_n)));
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
@@ -576,6 +761,13 @@ hipError_t launch_rows(const Fp8Product& p, hipStream_t stream) {
 }
 
 template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
+hipError_t launch_pipe(const Fp8Product& p, hipStream_t stream) {
+  return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 grid) {
+    hipLaunchKernelGGL((fp8_gemm_pipe_kernel<BM, BN, WM, WN, NS, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
+  });
+}
+
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
 hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
   return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 grid) {
     hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, NS, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
@@ -586,8 +778,8 @@ hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
 // as long as there are about two of them a CU at most; from there on tiles
 // through LDS, by their estimated time.
 // (us, K = 4096: M = 16, N = 1024 / 4096 / 14336: rows<1, 1> 4.6 / 6.4 / 17.0, rows<1, 2> 5.7 / 7.5 (8 waves), - / - / 14.6
-// (4); M = 32, N = 4096: rows<2, 1> 7.8, rows<2, 2> 9.9; M = 64, N = 4096: rows<2, 2> of 8 waves 9.8, of 4 10.4, 64 x 64 tiles
-// 15.6; M = 128, N = 4096: 17.0, 14.3, 15.7; M = 64, N = 14336: rows<2, 2> 27.9, 64 x 64 tiles 17.2.)
+// (4); M = 32, N = 4096: rows<2, 1> 7.8, rows<2, 2> 9.9; M = 64, N = 4096: rows<2, 2> of 8 waves 9.8, 32 x 64 tiles 12.2; M =
+// 128, N = 4096: rows<2, 2> of 4 waves 14.3, 32 x 64 tiles 12.6, to fp32 14.3 and 18.9, 64 x 64 tiles 18.1.)
 hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
   const auto tiles = [&](int64_t bm, int64_t bn) { return (p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
   if (p.M <= 16) {
@@ -597,26 +789,34 @@ hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
   const int64_t t = tiles(32, 16);
   if (t <= 256) return launch_rows<2, 1, 4, 4>(p, stream);
   if (t <= 512) return launch_rows<2, 2, 8, 2>(p, stream);
-  if (t <= 1024) return launch_rows<2, 2, 4, 2>(p, stream);
+  if (!p.bf16 && t <= 1024) return launch_rows<2, 2, 4, 2>(p, stream);
   // Time of a step (a block of 128 columns of all tiles), in us: that of the
   // rounds of workgroups that the 256 CUs take, one or two a CU; measured at K =
-  // 4096 and 14336 on M = 64 .. 4096, N = 1024 .. 14336.
+  // 4096 and 14336 on M = 32 .. 8192, N = 1024 .. 14336, where the choice is
+  // within 8% of the best (us at K = 4096 in the order below, to bf16: 128 x 4096
+  // 12.9 / 13.3 / 19.1 / 23.5 / 34.2 / 44.4; 256 x 4096 16.1 / 13.5 / 19.0 / 23.5 / 33.9
+  // / 48.6; 512 x 14336 97 / 70 / 57 / 42.1 / 37.5 / 49.8; 1024 x 4096 56 / 40.4 / 29.7 /
+  // 25.0 / 34.2 / 49; 4096 x 4096 202 / 138 / 111 / 78 / 77 / 62.5; to fp32: 512 x 4096
+  // 27.8 / 25.6 / 37.2; 2048 x 4096 99.5 / 83.6 / 64.9).
   const auto one = [&](int bm, int bn, double us) { return (double)((tiles(bm, bn) + 255) / 256) * us; };
   const auto two = [&](int bm, int bn, double alone, double both) {
     return tiles(bm, bn) <= 256 ? alone : (double)((tiles(bm, bn) + 511) / 512) * both;
   };
   if (!p.bf16) {
-    if (two(64, 128, 0.8, 1.3) < two(128, 128, 1.2, 2.0)) return launch_tile<64, 128, 2, 2, 2, true>(p, stream);
+    const double t64 = two(64, 64, 0.47, 0.78), t64x128 = two(64, 128, 0.73, 1.3), t128 = two(128, 128, 1.15, 2.0);
+    if (t64 <= t64x128 && t64 <= t128) return launch_pipe<64, 64, 2, 2, 4, true>(p, stream);
+    if (t64x128 <= t128) return launch_pipe<64, 128, 2, 2, 3, true>(p, stream);
     return launch_tile<128, 128, 2, 2, 2, true>(p, stream);
   }
-  const double t64 = two(64, 64, 0.47, 0.66), t64x128 = two(64, 128, 0.53, 0.95), t128 = two(128, 128, 0.73, 1.25),
-               t128x256 = one(128, 256, 1.15), t256 = one(256, 256, 1.9);
-  const double best = std::min({t64, t64x128, t128, t128x256, t256});
+  const double t32 = two(32, 64, 0.30, 0.46), t64 = two(64, 64, 0.33, 0.64), t64x128 = two(64, 128, 0.5, 0.88),
+               t128 = two(128, 128, 0.66, 1.15), t128x256 = one(128, 256, 1.07), t256 = one(256, 256, 1.8);
+  const double best = std::min({t32, t64, t64x128, t128, t128x256, t256});
   if (best == t256) return launch_tile<256, 256, 4, 2, 2, false>(p, stream);
   if (best == t128x256) return launch_tile<128, 256, 2, 4, 3, false>(p, stream);
   if (best == t128) return launch_tile<128, 128, 2, 2, 2, false>(p, stream);
-  if (best == t64x128) return launch_tile<64, 128, 2, 2, 3, false>(p, stream);
-  return launch_tile<64, 64, 2, 1, 4, false>(p, stream);
+  if (best == t64x128) return launch_pipe<64, 128, 2, 2, 3, false>(p, stream);
+  if (best == t64) return launch_pipe<64, 64, 2, 2, 4, false>(p, stream);
+  return launch_pipe<32, 64, 1, 2, 5, false>(p, stream);
 }
 
 }  // namespace nvfp4

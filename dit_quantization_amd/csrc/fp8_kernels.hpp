@@ -28,6 +28,7 @@ struct Fp8Product {
   int N, K;
   void* y;
   bool bf16;
+  int group = 0;  // of the launch: tiles of x that an XCD's stretch of tiles covers
 };
 
 hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t rows, int64_t cols, uint8_t* codes,
