@@ -57,15 +57,17 @@ struct Fragment8 {
   __device__ __forceinline__ i32x8 raw() const {
     return i32x8{(int)q[0].x, (int)q[0].y, (int)q[0].z, (int)q[0].w, (int)q[1].x, (int)q[1].y, (int)q[1].z, (int)q[1].w};
   }
+  // widened: operand h of the 4 bf16 matrix instructions of the 128 columns
+  __device__ __forceinline__ bf16x8 quarter(int h) const {
+    return widen8(q[h / 2][2 * (h & 1)], q[h / 2][2 * (h & 1) + 1]);
+  }
   // the 16 x 16 sums of 128 products, this operand's rows first
   __device__ __forceinline__ f32x4 times(const Fragment8& o) const {
     f32x4 d = {0, 0, 0, 0};
     if constexpr (WIDE) {
 #pragma unroll
       for (int h = 0; h < 4; ++h)
-        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            widen8(q[h / 2][2 * (h & 1)], q[h / 2][2 * (h & 1) + 1]),
-            widen8(o.q[h / 2][2 * (h & 1)], o.q[h / 2][2 * (h & 1) + 1]), d, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(quarter(h), o.quarter(h), d, 0, 0, 0);
     } else {
       d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(raw(), o.raw(), d, 0, 0, 0, 0, 0, 0);
     }
@@ -600,7 +602,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 // Small tiles: the fragments of two blocks fit the registers, so the next
 // block's are read while this one's are multiplied, and a step meets once.
 // 333 x 5000 x 4112 with 64 x 128 tiles, the kernel above and this one: 27.2 and
-// 22.9 us to bf16, 33.7 and 26.8 to fp32.
+// 22.9 us to bf16, 33.7 and 27.8 to fp32.
 template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
 __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_pipe_kernel(Fp8Product p) {
   using Tile = TileOf<BM, BN, WM, WN>;
@@ -653,6 +655,18 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   };
   const auto load_scales = [&](int set, int b) { t.read_scales(st.scales[(b >> 2) & 1], b, xsc[set], wsc[set]); };
 
+  // WIDE: the fragments widened, a quarter (one matrix instruction's operand) at a
+  // time and ahead of the tiles that want them (300 x 4096 x 14336 76.2 -> 73.4 us):
+  // in a step its W_1 .., then the next one's W_0 and X.
+  bf16x8 ww[WIDE ? TN : 1][4], xw[2][WIDE ? TM : 1][4];
+  constexpr int UNITS = 4 * (TM + TN);
+  const auto widen = [&](int set, int u) {
+    const int f = u / 4 + 1, h = u % 4;
+    if (f < TN) ww[f][h] = wf[set][f].quarter(h);
+    else if (f == TN) ww[0][h] = wf[set ^ 1][0].quarter(h);
+    else xw[set ^ 1][f - TN - 1][h] = xf[set ^ 1][f - TN - 1].quarter(h);
+  };
+
   f32x4 acc[TN][TM];
 #pragma unroll
   for (int i = 0; i < TN; ++i)
@@ -691,7 +705,18 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       for (int r = RT * q; r < RT * (q + 1) && r < READS; ++r) read(set ^ 1, stage, r);
 #pragma unroll
       for (int l = LT * q; l < LT * (q + 1) && l < LOADS; ++l) dma(free, b + NS, l);
-      d[q % 4] = wf[set][q / TM].times(xf[set][q % TM]);
+      if constexpr (WIDE) {
+        constexpr int UT = (UNITS + TILES - 1) / TILES;
+        f32x4 e = {0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          e = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww[q / TM][h], xw[set][q % TM][h], e, 0, 0, 0);
+        d[q % 4] = e;
+#pragma unroll
+        for (int u = UT * q; u < UT * (q + 1) && u < UNITS; ++u) widen(set, u);
+      } else {
+        d[q % 4] = wf[set][q / TM].times(xf[set][q % TM]);
+      }
       if (q >= LAG) add(q - LAG, s[(q - LAG) % TM]);
       else add(TILES + q - LAG, q == LAG - 1 ? s_last : s_last2);
       __builtin_amdgcn_sched_barrier(0);
@@ -708,6 +733,10 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   load_scales(0, 0);
 #pragma unroll
   for (int r = 0; r < READS; ++r) read(0, 0, r);
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int u = UNITS - 4 * (TM + 1); u < UNITS; ++u) widen(1, u);
+  }
 #pragma unroll
   for (int j = 0; j < TM; ++j) s[j] = 0.0f;
   int b = 0, stage = 0;
