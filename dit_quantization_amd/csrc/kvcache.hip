@@ -3,7 +3,11 @@
 //
 // A workgroup has some tokens of one of the two tensors.  First a thread a
 // token finds its place (a search in cu and one page number), then all threads
-// move the tokens' heads, several vectors in flight each.
+// move the tokens' heads, several vectors in flight each.  Memory bounds both
+// where there are many tokens (65536 tokens of 8 heads of 128, bf16: written
+// in 91 us, 4.5 TB/s, read in 87, 4.7), and below about a thousand the launch
+// and the three reads that follow each other (cu, page number, codes): 4.5 us.
+// Found once a workgroup the places cost 87 us, found by every thread 137.
 #include "device_common.hpp"
 #include "encode8.hpp"
 #include "fp8_kernels.hpp"
@@ -64,8 +68,9 @@ __device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b, uint32_t per)
   return q + (a - q * b >= b ? 1 : 0);
 }
 
-// A row is one token and head; T lanes have it, 16 elements each, and U rows at
-// a time.
+// A row is one token and head; T lanes have it, 16 elements each (8191 tokens of
+// 8 heads of 128, INT8: 13.7 us, with 8 elements 16.8), and U rows at a time.
+// The maximum is fp32's, exact; the quotients are decided as encode8.hpp says.
 template <bool BF, int T, int U>
 __global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3,
                                                         int64_t first, int per_block, uint32_t per_head) {
@@ -124,10 +129,12 @@ __global__ __launch_bounds__(256) void kv8_write_kernel(kv8_tensor keys, kv8_ten
   }
 }
 
-// A thread has 16 elements of a head, U times.
+// A thread has 16 elements of a head, U times.  scale * code is rounded to fp32
+// once and from there to bf16, as the definition has it.
 template <bool BF, int U>
 __global__ __launch_bounds__(256) void kv8_read_kernel(kv8_tensor keys, kv8_tensor values, kv8_places p, bool e4m3,
-                                                       int64_t first, int per_block, uint32_t per_k, uint32_t per_v, uint32_t per_head) {
+                                                       int64_t first, int per_block, uint32_t per_k, uint32_t per_v,
+                                                       uint32_t per_head) {
   __shared__ Places places;
   const kv8_tensor& c = blockIdx.y ? values : keys;
   const uint32_t units = (uint32_t)c.dim / 16, per_unit = blockIdx.y ? per_v : per_k;
@@ -163,7 +170,8 @@ __global__ __launch_bounds__(256) void kv8_read_kernel(kv8_tensor keys, kv8_tens
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (e4m3) {
-          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], true);
+          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], false);
+          const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(q[u][j], true);
           v[4 * j] = a.x * s[u], v[4 * j + 1] = a.y * s[u], v[4 * j + 2] = b.x * s[u], v[4 * j + 3] = b.y * s[u];
         } else {
 #pragma unroll
@@ -202,7 +210,9 @@ hipError_t launch_kv8(const kv8_tensor& keys, const kv8_tensor& values, const kv
   };
   if (!write) {
     return launch(p.heads * (dim / 16), [&](dim3 g, int u, int64_t first, int n) {
-#define READ_CASE(BF, U)                                                                                          hipLaunchKernelGGL((kv8_read_kernel<BF, U>), g, dim3(256), 0, stream, keys, values, p, e4m3, first, n,                             per(keys.dim / 16), per(values.dim / 16), per_head)
+#define READ_CASE(BF, U)                                                                                   \
+  hipLaunchKernelGGL((kv8_read_kernel<BF, U>), g, dim3(256), 0, stream, keys, values, p, e4m3, first, n,    \
+                     per(keys.dim / 16), per(values.dim / 16), per_head)
       if (bf16 && u == 4) READ_CASE(true, 4);
       else if (bf16) READ_CASE(true, 1);
       else if (u == 4) READ_CASE(false, 4);

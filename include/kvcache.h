@@ -14,8 +14,8 @@
  * 0; code = nearest value to v / scale (exact quotient), ties to even.
  *
  * Places: the calls work on `tokens` rows that belong to `seqs` sequences.
- * Rows cu[b] .. cu[b + 1] - 1 belong to sequence b (int32 cu [seqs + 1],
- * non-decreasing); row t is the sequence's position p = starts[b] + t - cu[b]
+ * Rows cu[b] .. cu[b + 1] - 1 belong to sequence b (int32 cu [seqs + 1], none
+ * negative, non-decreasing); row t is the sequence's position p = starts[b] + t - cu[b]
  * (int32 starts [seqs], or NULL for 0), which lies in row p % page_size of page
  * page_table[b, p / page_size] (int32 [seqs, table_width], contiguous). Rows
  * before cu[0] and from cu[seqs] on belong to no sequence. A position below 0

@@ -283,6 +283,53 @@ def test_gemm_scales_at_the_ends_of_fp32(M):
             check_product(fp8.gemm(x, xs, w, ws, out_dtype=dtype), x, xs, w, ws)
 
 
+# A size for each of the launcher's kernels (16, 32, 64, 128 and 256 rows of x a
+# workgroup, with N that allows 16-byte stores and that does not).
+TILES = [(7, 9001), (9, 8904), (33, 4144), (131, 2137), (390, 1411), (40, 8400), (270, 6005), (700, 2056), (201, 8301),
+         (513, 5016), (390, 9349), (1100, 6008), (1156, 6805), (900, 8752)]
+
+
+@pytest.mark.parametrize("M,N", TILES)
+def test_gemm_tiles(M, N):
+    """1 to 6, 8 and 9 blocks of columns, the last one short or not: every remainder of a kernel's stages."""
+    for K in (16, 144, 272, 384, 528, 656, 1024, 1040):
+        print(f"[case] gemm tiles {M}x{N}x{K}", flush=True)
+        x, w = operand(M, K, 31, "plain"), operand(N, K, 32, "plain")
+        G = -(-K // 128)
+        xs, ws = scales(M, G, seed=33), scales(-(-N // 128), G, seed=34)
+        for dtype in (BF, FL):
+            whole = torch.full((M * N + 64,), 5.0, dtype=dtype, device=DEV)
+            y = fp8.gemm(x, xs, w, ws, out=whole[:M * N].view(M, N))
+            check_product(y, x, xs, w, ws)
+            assert bool((whole[M * N:] == 5.0).all())
+
+
+@pytest.mark.parametrize("M,N", TILES)
+def test_gemm_tiles_with_scales_at_the_ends_of_fp32(M, N):
+    """In one of four blocks, and another one's every third row, the product of
+    the scales is 2^-127, below fp32's normal numbers, elsewhere 2^-126."""
+    K = 400
+    x, w = operand(M, K, 35, "plain"), operand(N, K, 36, "plain")
+    xs, ws = torch.full((M, 4), 2.0 ** -60, device=DEV), torch.full((-(-N // 128), 4), 2.0 ** -66, device=DEV)
+    xs[:, 1], ws[:, 1] = 2.0 ** -120, 2.0 ** -7
+    xs[:, 2], ws[:, 2] = 2.0 ** 13, 2.0 ** -139
+    xs[::3, 2] = 2.0 ** 12
+    k = torch.arange(K, device=DEV) // 128
+    X = x.double() * (xs.double() * 2.0 ** 60)[:, k]
+    W = w.double() * (ws.double() * 2.0 ** 66)[torch.arange(N, device=DEV) // 128][:, k]
+    ystar, a = X @ W.t().contiguous(), X.abs() @ W.abs().t().contiguous()
+    for dtype in (BF, FL):
+        y = fp8.gemm(x, xs, w, ws, out_dtype=dtype).double() * 2.0 ** 126
+        # as check_product, and half a step of fp32's smallest numbers, 2^-150, for the blocks' sums (four) and
+        # their additions, of bf16's, 2^-134, for the result
+        tau = (K + 4) * U32 * a + 8 * 2.0 ** (126 - 150)
+        if dtype == BF:
+            tau = tau + 7 * 2.0 ** -13 * a
+            tau = tau * (1 + HALF_BF16) + HALF_BF16 * ystar.abs() + 2.0 ** (126 - 134)
+        bad = (y - ystar).abs() > tau
+        assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outputs"
+
+
 def test_gemm_longest_rows():
     """K = 2^22, the most the call takes: sums of 2^22 products in every tile kernel."""
     K = 1 << 22
