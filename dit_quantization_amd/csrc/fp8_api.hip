@@ -84,7 +84,7 @@ int fp8_gemm(const uint8_t* x, const float* x_scales, const uint8_t* w, const fl
   hipStream_t s;
   if (const int st = begin(stream, &s); st != NVFP4_OK) return st;
   return launch_status(
-      launch_fp8_gemm({x, x_scales, w, w_scales, M, (int)N, (int)K, y, y_dtype == NVFP4_BF16}, s));
+      launch_fp8_gemm({x, x_scales, w, w_scales, M, (int)N, (int)K, y, N, y_dtype == NVFP4_BF16}, s));
 }
 
 }  // extern "C"

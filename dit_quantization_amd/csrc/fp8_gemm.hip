@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (n + r >= p.N) break;
-        const int64_t at = (m0 + m) * p.N + n + r;
+        const int64_t at = (m0 + m) * p.y_stride + n + r;
         if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)f32_to_bf16_bits(v[r]);
         else reinterpret_cast<float*>(p.y)[at] = v[r];
       }
@@ -378,10 +378,11 @@ struct TileOf {
     // A lane has, of a tile, one row of x and four rows of the weight.  bf16
     // rows go through LDS (a wave's own part of the stages, 16-byte chunks
     // swizzled by the row) and out as 16 bytes a lane, non-temporal: y is not
-    // read again here.
+    // read again here.  (Where y's rows are a multiple of 8 long, so is p.N: a part's
+    // columns are whole tiles, or the rest of a row.)
     constexpr int RC = WBN / 8;  // 16-byte chunks of a wave's bf16 rows
     const int nw = n0 + wn * WBN;
-    if (p.bf16 && (p.N & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
+    if (p.bf16 && (p.y_stride & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
       static_assert(WBM * WBN * 2 * NW <= LDS && WBM * RC % 64 == 0, "the tile fits the stages");
       __builtin_amdgcn_s_barrier();  // every wave has read the stages (its reads are waited for above)
       uint32_t* out = reinterpret_cast<uint32_t*>(lds) + wave * (WBM * WBN / 2);
@@ -403,11 +404,12 @@ struct TileOf {
         const int m = (64 * q + lane) / RC, c = lane & (RC - 1);
         const u32x4 v = *reinterpret_cast<const u32x4*>(out + (m * RC + (c ^ (m & 15 & (RC - 1)))) * 4);
         const int row = wm * WBM + m, n = nw + 8 * c;
-        if (row < rows && n < p.N) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (m0 + row) * p.N + n));
+        if (row < rows && n < p.N)
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(y + (m0 + row) * p.y_stride + n));
       }
       return;
     }
-    const bool fours = !p.bf16 && (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+    const bool fours = !p.bf16 && (p.y_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int m = wm * WBM + 16 * j + l16;
@@ -415,7 +417,7 @@ struct TileOf {
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         const int n = nw + 16 * i + 4 * g;
-        const int64_t at = (m0 + m) * p.N + n;
+        const int64_t at = (m0 + m) * p.y_stride + n;
         if (fours) {
           if (n < p.N) __builtin_nontemporal_store(acc[i][j], reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.y) + at));
           continue;
@@ -782,7 +784,7 @@ hipError_t launch_tiles(const Fp8Product& all, int bm, int bn, F launch) {
     p.M = all.M - m0 < step ? all.M - m0 : step;
     p.x += m0 * all.K;
     p.xs += m0 * ((all.K + 127) / 128);
-    p.y = reinterpret_cast<char*>(all.y) + m0 * all.N * (all.bf16 ? 2 : 4);
+    p.y = reinterpret_cast<char*>(all.y) + m0 * all.y_stride * (all.bf16 ? 2 : 4);
     p.group = group_of((p.M + bm - 1) / bm, tiles_n, bm, bn);
     launch(p, dim3((unsigned)((p.M + bm - 1) / bm * tiles_n)));
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
@@ -811,6 +813,86 @@ hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
   });
 }
 
+// Kernels of many rows, and the time of a step (a block of 128 columns of all
+// tiles) of theirs in us: that of the rounds of workgroups that the 256 CUs take,
+// one a CU, or where `both` is given two; measured at K = 4096 and 14336 on M = 32 ..
+// 8192, N = 1024 .. 14336, where the choice is within 8% of the best (us at K =
+// 4096 in the order below, to bf16: 128 x 4096 12.9 / 13.3 / 19.1 / 23.5 / 34.2 / 44.4;
+// 256 x 4096 16.1 / 13.5 / 19.0 / 23.5 / 33.9 / 48.6; 512 x 14336 97 / 70 / 57 / 42.1 /
+// 37.5 / 49.8; 1024 x 4096 56 / 40.4 / 29.7 / 25.0 / 34.2 / 49; 4096 x 4096 202 / 138 /
+// 111 / 78 / 77 / 62.5; to fp32: 512 x 4096 27.8 / 25.6 / 37.2; 2048 x 4096 99.5 / 83.6 /
+// 64.9).
+struct TileKernel {
+  int bm, bn;
+  double alone, both;
+  hipError_t (*launch)(const Fp8Product&, hipStream_t);
+  int64_t tiles_m(int64_t M) const { return (M + bm - 1) / bm; }
+  int64_t tiles_n(int64_t N) const { return (N + bn - 1) / bn; }
+  double step(int64_t M, int64_t N) const {
+    const int64_t t = tiles_m(M) * tiles_n(N);
+    return both > 0 && t > 256 ? (double)((t + 511) / 512) * both : (double)((t + 255) / 256) * alone;
+  }
+};
+const TileKernel kTiles16[] = {{32, 64, 0.30, 0.46, launch_pipe<32, 64, 1, 2, 5, false>},
+                               {64, 64, 0.33, 0.64, launch_pipe<64, 64, 2, 2, 4, false>},
+                               {64, 128, 0.50, 0.88, launch_pipe<64, 128, 2, 2, 3, false>},
+                               {128, 128, 0.66, 1.15, launch_tile<128, 128, 2, 2, 2, false>},
+                               {128, 256, 1.07, 0.0, launch_tile<128, 256, 2, 4, 3, false>},
+                               {256, 256, 1.80, 0.0, launch_tile<256, 256, 4, 2, 2, false>}};
+const TileKernel kTiles32[] = {{64, 64, 0.47, 0.78, launch_pipe<64, 64, 2, 2, 4, true>},
+                               {64, 128, 0.73, 1.30, launch_pipe<64, 128, 2, 2, 3, true>},
+                               {128, 128, 1.15, 2.00, launch_tile<128, 128, 2, 2, 2, true>}};
+
+// The kernel of the least estimated time, or two: whole rounds of one with one
+// workgroup a CU for the first columns or rows and the best for the rest, where
+// that looks 5% better or more (1000 x 20000 x 4096: 1.2 rounds of 256 x 256 tiles
+// 119 us, one round and one of 128 x 128 88; 6000 x 4096 x 4096 107 and 99; 4096 x
+// 14336 x 4096, 3.5 rounds, 226 and 224: the clock is at its power limit. Two
+// workgroups a CU do not end together: 2048 x 14336 x 4096 to fp32 245 and 255).
+hipError_t launch_tiled(const Fp8Product& p, hipStream_t stream) {
+  const TileKernel* all = p.bf16 ? kTiles16 : kTiles32;
+  const int n = p.bf16 ? 6 : 3;
+  const auto best = [&](int64_t M, int64_t N, double& us) {
+    const TileKernel* b = all;
+    us = b->step(M, N);
+    for (int i = 1; i < n; ++i)
+      if (const double t = all[i].step(M, N); t < us) us = t, b = all + i;
+    return b;
+  };
+  double us;
+  const TileKernel *first = best(p.M, p.N, us), *second = nullptr;
+  int64_t M1 = p.M, N1 = p.N;
+  const double apart = 3.0 * 128 / (double)p.K;  // of a second launch
+  us *= 0.95;
+  for (int i = 0; i < n; ++i) {
+    const TileKernel& k = all[i];
+    const int64_t tm = k.tiles_m(p.M), tn = k.tiles_n(p.N), whole = tm * tn / 256 * 256;
+    if (k.both > 0 || whole == 0) continue;
+    const auto consider = [&](int64_t M, int64_t N, int64_t M2, int64_t N2) {
+      if (M == 0 || N == 0 || M2 <= 0 || N2 <= 0) return;
+      double rest;
+      const TileKernel* b = best(M2, N2, rest);
+      if (const double t = k.step(M, N) + rest + apart; t < us) us = t, first = &k, second = b, M1 = M, N1 = N;
+    };
+    consider(p.M, whole / tm * k.bn, p.M, p.N - whole / tm * k.bn);  // (bn is a multiple of 128)
+    consider(whole / tn * k.bm, p.N, p.M - whole / tn * k.bm, p.N);
+  }
+  Fp8Product a = p;
+  a.M = M1;
+  a.N = (int)N1;
+  if (const hipError_t e = first->launch(a, stream); e != hipSuccess || !second) return e;
+  const int64_t G = (p.K + 127) / 128, m = M1 < p.M ? M1 : 0, c = N1 < p.N ? N1 : 0;
+  a = p;
+  a.M -= m;
+  a.N -= (int)c;
+  a.x += m * p.K;
+  a.xs += m * G;
+  a.w += c * p.K;
+  a.ws += c / 128 * G;
+  a.y = reinterpret_cast<char*>(p.y) + (m * p.y_stride + c) * (p.bf16 ? 2 : 4);
+  return second->launch(a, stream);
+}
+
 // Few rows in all: workgroups of few waves that share nothing but their sums,
 // as long as there are about two of them a CU at most; from there on tiles
 // through LDS, by their estimated time.
@@ -827,33 +909,7 @@ hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
   if (t <= 256) return launch_rows<2, 1, 4, 4>(p, stream);
   if (t <= 512) return launch_rows<2, 2, 8, 2>(p, stream);
   if (!p.bf16 && t <= 1024) return launch_rows<2, 2, 4, 2>(p, stream);
-  // Time of a step (a block of 128 columns of all tiles), in us: that of the
-  // rounds of workgroups that the 256 CUs take, one or two a CU; measured at K =
-  // 4096 and 14336 on M = 32 .. 8192, N = 1024 .. 14336, where the choice is
-  // within 8% of the best (us at K = 4096 in the order below, to bf16: 128 x 4096
-  // 12.9 / 13.3 / 19.1 / 23.5 / 34.2 / 44.4; 256 x 4096 16.1 / 13.5 / 19.0 / 23.5 / 33.9
-  // / 48.6; 512 x 14336 97 / 70 / 57 / 42.1 / 37.5 / 49.8; 1024 x 4096 56 / 40.4 / 29.7 /
-  // 25.0 / 34.2 / 49; 4096 x 4096 202 / 138 / 111 / 78 / 77 / 62.5; to fp32: 512 x 4096
-  // 27.8 / 25.6 / 37.2; 2048 x 4096 99.5 / 83.6 / 64.9).
-  const auto one = [&](int bm, int bn, double us) { return (double)((tiles(bm, bn) + 255) / 256) * us; };
-  const auto two = [&](int bm, int bn, double alone, double both) {
-    return tiles(bm, bn) <= 256 ? alone : (double)((tiles(bm, bn) + 511) / 512) * both;
-  };
-  if (!p.bf16) {
-    const double t64 = two(64, 64, 0.47, 0.78), t64x128 = two(64, 128, 0.73, 1.3), t128 = two(128, 128, 1.15, 2.0);
-    if (t64 <= t64x128 && t64 <= t128) return launch_pipe<64, 64, 2, 2, 4, true>(p, stream);
-    if (t64x128 <= t128) return launch_pipe<64, 128, 2, 2, 3, true>(p, stream);
-    return launch_tile<128, 128, 2, 2, 2, true>(p, stream);
-  }
-  const double t32 = two(32, 64, 0.30, 0.46), t64 = two(64, 64, 0.33, 0.64), t64x128 = two(64, 128, 0.5, 0.88),
-               t128 = two(128, 128, 0.66, 1.15), t128x256 = one(128, 256, 1.07), t256 = one(256, 256, 1.8);
-  const double best = std::min({t32, t64, t64x128, t128, t128x256, t256});
-  if (best == t256) return launch_tile<256, 256, 4, 2, 2, false>(p, stream);
-  if (best == t128x256) return launch_tile<128, 256, 2, 4, 3, false>(p, stream);
-  if (best == t128) return launch_tile<128, 128, 2, 2, 2, false>(p, stream);
-  if (best == t64x128) return launch_pipe<64, 128, 2, 2, 3, false>(p, stream);
-  if (best == t64) return launch_pipe<64, 64, 2, 2, 4, false>(p, stream);
-  return launch_pipe<32, 64, 1, 2, 5, false>(p, stream);
+  return launch_tiled(p, stream);
 }
 
 }  // namespace nvfp4

@@ -27,6 +27,7 @@ struct Fp8Product {
   int64_t M;
   int N, K;
   void* y;
+  int64_t y_stride;  // N of the whole product: a launch may have some of its columns
   bool bf16;
   int group = 0;  // of the launch: tiles of x that an XCD's stretch of tiles covers
 };
