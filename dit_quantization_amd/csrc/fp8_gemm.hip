@@ -321,14 +321,15 @@ struct TileOf {
     w = of[4 * (64 * XSW + wn * WBN / 128)];
   }
   // Those that are no normal number count as 0 (see other_blocks).
+  static __device__ __forceinline__ void factor(float x, float w, float& s, bool& odd) {
+    const float v = x * w;
+    const bool o = not_normal(v);
+    s = o ? 0.0f : v;
+    odd |= o;
+  }
   static __device__ __forceinline__ void factors(const float (&x)[TM], float w, float (&s)[TM], bool& odd) {
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const float v = x[j] * w;
-      const bool o = not_normal(v);
-      s[j] = o ? 0.0f : v;
-      odd |= o;
-    }
+    for (int j = 0; j < TM; ++j) factor(x[j], w, s[j], odd);
   }
 
   // Products of scales that are no normal number could leave fp32's range
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   const auto load_x = [&](int stage, int j, int h) { xf[j].q[h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
   const auto load_w = [&](int stage, int i, int h) { wf[i % WB].q[h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
   const auto load_scales = [&](int b) { t.read_scales(st.scales[(b >> 2) & 1], b, xsc, wsc); };
-  const auto factors = [&] { Tile::factors(xsc, wsc, s, odd); };
+  const auto factor = [&](int j) { Tile::factor(xsc[j], wsc, s[j], odd); };
 
   f32x4 acc[TN][TM];
 #pragma unroll
@@ -510,10 +511,14 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       acc[tile_i(q)][tile_j(q)][r] = __builtin_fmaf(d[q % 4][r], f, acc[tile_i(q)][tile_j(q)][r]);
   };
   static_assert(TILES % 4 == 0 && LAG <= LAST, "d's entries follow the tiles; the last two tiles share a factor");
-  const auto tile = [&](int q) {
+  const auto multiply_tile = [&](int q) {
     d[q % 4] = multiply(tile_i(q), tile_j(q));
+    if (!WIDE) __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto add_tile = [&](int q) {
     if (q >= LAG) add(q - LAG, s[tile_j(q - LAG)]);
     else add(TILES + q - LAG, s_last);
+    __builtin_amdgcn_sched_barrier(0);
   };
   // All waves are past their reads of what the next loads overwrite, and all
   // loads but the newest `n` a wave have landed.
@@ -530,38 +535,44 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   constexpr int A = TN / 2 - 2;
   constexpr int SLACK = L1 + 1 + L2;  // loads of a block, one for scales among them
   static_assert((NS - 1) * SLACK + L2 <= 63, "the counter of loads in flight");
+  // (The matrix instruction goes first in a tile, so that it is issued right behind a meet.)
   const auto step = [&](int b, int cur) {
     const int nxt = (cur + 1) % NS;
 #pragma unroll
     for (int q = 0; q < T0; ++q) {
       const int i = q / TM, c = q % TM;
       if (q == A * TM) meet(std::integral_constant<int, (NS - 1) * SLACK>{});
+      multiply_tile(q);
       if (c < 2) load_w(cur, i + 2, c);
-      if (q >= A * TM && q - A * TM < L1) dma(cur, b + NS, q - A * TM);
-      if (q == T0 - 1) dma_scales(b + NS);
-      tile(q);
-      __builtin_amdgcn_sched_barrier(0);
-    }
 #pragma unroll
-    for (int q = T0 - A * TM; q < L1; ++q) dma(cur, b + NS, q);
+      for (int l = 0; l < L1; ++l)
+        if (q == A * TM + l * (T0 - A * TM) / L1) dma(cur, b + NS, l);
+      if (q == T0 - 1) dma_scales(b + NS);
+      add_tile(q);
+    }
     meet(std::integral_constant<int, (NS - 1) * SLACK>{});
-    load_scales(b + 1);
 #pragma unroll
     for (int q = T0; q < TILES; ++q) {
       const int c = (q - T0) / LAST, in_c = (q - T0) % LAST;
-      if (q - T0 < L2) dma(cur, b + NS, L1 + q - T0);
-      tile(q);
+      multiply_tile(q);
+      if (q == T0) load_scales(b + 1);
       if (q - T0 < 4) load_w(nxt, (q - T0) / 2, (q - T0) % 2);
       if (in_c == LAST - 1) {
         load_x(nxt, c, 0);
         load_x(nxt, c, 1);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
 #pragma unroll
-    for (int q = TILES - T0; q < L2; ++q) dma(cur, b + NS, L1 + q);
-    s_last = s[TM - 1];
-    factors();
+      for (int l = 0; l < L2; ++l)
+        if (q == T0 + l * (TILES - T0) / L2) dma(cur, b + NS, L1 + l);
+      add_tile(q);
+      // a column's factor, once its last sums have been added
+      if (q == T0 + 2) {
+        s_last = s[TM - 1];
+        factor(TM - 1);
+      }
+      if (in_c == LAST - 1 && c >= 2) factor(c - 2);
+    }
+    factor(TM - 2);
   };
   static_assert(TM >= 2, "a tile a fragment's load");
 
@@ -582,7 +593,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     load_w(0, 0, h);
     load_w(0, 1, h);
   }
-  factors();
+#pragma unroll
+  for (int j = 0; j < TM; ++j) factor(j);
   int b = 0;
   for (; b + NS <= G; b += NS) {
     step(b, 0);
@@ -704,17 +716,9 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
     __builtin_amdgcn_sched_barrier(0);
     const int free = stage;
     stage = stage + 1 == NS ? 0 : stage + 1;
-    s_last = s[TM - 1];
-    s_last2 = s[TM - 2];
-    Tile::factors(xsc[set], wsc[set], s, odd);
-    load_scales(set ^ 1, b + 1);
 #pragma unroll
     for (int q = 0; q < TILES; ++q) {
       constexpr int RT = (READS + TILES - 1) / TILES, LT = (LOADS + TILES - 1) / TILES;
-#pragma unroll
-      for (int r = RT * q; r < RT * (q + 1) && r < READS; ++r) read(set ^ 1, stage, r);
-#pragma unroll
-      for (int l = LT * q; l < LT * (q + 1) && l < LOADS; ++l) dma(free, b + NS, l);
       if constexpr (WIDE) {
         constexpr int UT = (UNITS + TILES - 1) / TILES;
         f32x4 e = {0, 0, 0, 0};
@@ -727,6 +731,17 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       } else {
         d[q % 4] = wf[set][q / TM].times(xf[set][q % TM]);
       }
+      if (!WIDE) __builtin_amdgcn_sched_barrier(0);
+      if (q == 0) {
+        s_last = s[TM - 1];
+        s_last2 = s[TM - 2];
+        Tile::factors(xsc[set], wsc[set], s, odd);
+        load_scales(set ^ 1, b + 1);
+      }
+#pragma unroll
+      for (int r = RT * q; r < RT * (q + 1) && r < READS; ++r) read(set ^ 1, stage, r);
+#pragma unroll
+      for (int l = LT * q; l < LT * (q + 1) && l < LOADS; ++l) dma(free, b + NS, l);
       if (q >= LAG) add(q - LAG, s[(q - LAG) % TM]);
       else add(TILES + q - LAG, q == LAG - 1 ? s_last : s_last2);
       __builtin_amdgcn_sched_barrier(0);
