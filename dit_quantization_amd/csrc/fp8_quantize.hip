@@ -82,8 +82,8 @@ hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t
 // ---- activations.  A row is cut into slots of 16 columns, filled up to whole
 // groups, and slots go to threads in order, so that a group is 2, 4 or 8
 // neighbouring lanes.  4096 x 14336 bf16 to E4M3: 36 us, 4.9 TB/s; SiLU(gate) x
-// 71 us, 4.1 TB/s, where the fp64 arithmetic (a table's read, a product and a
-// quotient a value) and memory take about the same time.
+// 68 us, 4.4 TB/s: memory, and fp64 arithmetic (a table's read, a product and a
+// quotient a value) that would take half as long alone.
 
 // g / (1 + exp(-g)) to within 2^-45 of itself: exp(-g) = 2^n exp(r), |r| <= ln 2
 // / 2, by 12 terms of its series (the rest is below 2^-47), and a reciprocal of
@@ -105,14 +105,32 @@ __device__ __forceinline__ double silu64(float g) {
   return z * __builtin_fma(q, __builtin_fma(-d, q, 1.0), q);
 }
 
-// The same of a bf16 gate from a table in LDS: of both signs and all magnitudes
-// from 2^-16 up to 2^8.
+// The same of a bf16 gate from a table: of both signs and all magnitudes from
+// 2^-16 up to 2^8, computed when this file is compiled (within 2^-48: ln 2 in two
+// parts, 17 terms of the series).
 constexpr uint32_t kTableFirst = (127 - 16) << 7, kTableSize = 24 << 7;
-__device__ __forceinline__ void fill_table(double* table) {
-  for (uint32_t i = threadIdx.x; i < 2 * kTableSize; i += blockDim.x) {
-    const uint32_t bits = i < kTableSize ? kTableFirst + i : 0x8000u + kTableFirst + (i - kTableSize);
-    table[i] = silu64(bf16_bits_to_f32(bits));
+struct SiluTable {
+  double v[2 * kTableSize];
+  constexpr SiluTable() : v() {
+    constexpr double kLn2High = 0x1.62e42fefap-1, kLn2Low = 0x1.cf79abc9e3b3ap-40;  // 38 bits, and the rest
+    for (uint32_t i = 0; i < kTableSize; ++i) {
+      const double g = (double)__builtin_bit_cast(float, (kTableFirst + i) << 16);
+      const int n = (int)(g * 1.4426950408889634 + 0.5);
+      const double r = (n * kLn2High - g) + n * kLn2Low;  // exp(-g) = 2^-n exp(r), |r| <= ln 2 / 2
+      double e = 1.0;
+      for (int k = 17; k > 0; --k) e = 1.0 + e * r / k;
+      e *= __builtin_bit_cast(double, (uint64_t)(1023 - n) << 52);
+      v[i] = g / (1.0 + e);
+      v[kTableSize + i] = -g * e / (1.0 + e);
+    }
   }
+};
+__device__ constexpr SiluTable kSilu{};
+__device__ __forceinline__ void fill_table(double* table) {
+  static_assert(kTableSize % 512 == 0, "two entries a thread at a time");
+#pragma unroll
+  for (uint32_t i = 0; i < 2 * kTableSize; i += 2 * 512)
+    *reinterpret_cast<u32x4*>(table + i + 2 * threadIdx.x) = *reinterpret_cast<const u32x4*>(kSilu.v + i + 2 * threadIdx.x);
   __syncthreads();
 }
 
@@ -125,13 +143,14 @@ __device__ __forceinline__ T group_all(T v, int L, F f) {
   return v;
 }
 
-// TABLE (bf16 gates): a grid of as many workgroups as fit at once, each with
-// its own table.  For 8 million values and more: filling it costs 2 us, an
-// exponential 24 of 47 vector instructions a value.
+// TABLE (bf16 gates): a grid of as many workgroups as fit at once, each with a
+// copy of the table in LDS.  For 8 million values and more: an exponential is 24
+// of 47 vector instructions a value (4096 x 14336 68 against 98 us; 512 x 14336
+// 15.0 against 14.2, where copying the table takes longer than it saves).
 template <bool BF, bool SILU, bool TABLE>
 __global__ __launch_bounds__(TABLE ? 512 : 256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, uint32_t per,
                                                                               uint32_t all, double q, double inv_q) {
-  __shared__ double table[TABLE ? 2 * kTableSize : 1];
+  __shared__ __attribute__((aligned(16))) double table[TABLE ? 2 * kTableSize : 1];
   if (TABLE) fill_table(table);
   const int L = a.group / 16;
   // (rounds of whole workgroups, so that all lanes of a group are there)

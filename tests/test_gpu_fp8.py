@@ -150,6 +150,32 @@ def test_quantize_act_many(seed):
             assert np.array_equal(scales.cpu().numpy(), rs) and np.array_equal(values(codes), rc)
 
 
+@pytest.mark.parametrize("rows", [65536, 640])
+def test_quantize_act_every_gate(rows):
+    """All finite bf16 gates (a group each), or every hundredth: the scale has 24 bits of SiLU(gate) in every
+    group."""
+    bits = torch.arange(0, 65536, 65536 // rows, dtype=torch.int32, device=DEV)[:rows]
+    g = (bits << 16).view(FL)
+    g = torch.where(torch.isfinite(g), g, 0.0)
+    gate = g.to(BF)[:, None].expand(rows, 128).contiguous()
+    x = torch.ones(rows, 128, dtype=BF, device=DEV)
+    x[:, 1::2] = 0.8125
+    y = ref.silu_product(host(x), host(gate))
+    rc, rs = ref.quantize_groups(y, 32, True)
+    c, s = fp8.quantize_act(x, gate, group_size=32)
+    # Bit for bit but for scales that fp64 cannot decide (include/fp8.h: within 2^-44 of a border).  There are such:
+    # SiLU(g) = g/2 + g^2/4 - g^4/48 ..., and for g = 1.5 2^-24, say, (g/2 + g^2/4) / 448 = 2^-34 12/7 (1 + 0.75 2^-24)
+    # lies half way between two fp32 numbers (12/7 2^23 = .. + 6/7, and 12/7 2^23 0.75 2^-24 = 9/14, together 3/2), with
+    # the true value 2^-76 of itself below.
+    got, exact = host(s), np.abs(y).reshape(rows, 4, 32).max(2) / 448
+    off = got != rs
+    half_way = (got.astype(np.float64) + rs.astype(np.float64)) / 2
+    assert (np.abs(got.view(np.int32) - rs.view(np.int32))[off] == 1).all()
+    assert (np.abs(exact - half_way)[off] <= 2.0 ** -44 * exact[off]).all() and off.sum() < 64
+    # (the codes of these do not depend on which of the two scales it is)
+    assert np.array_equal(values(c), rc)
+
+
 def test_quantize_act_halves_of_a_product_and_only_its_outputs():
     F = 208
     h = tensor(rng(3).standard_normal((5, 2 * F)), BF)
