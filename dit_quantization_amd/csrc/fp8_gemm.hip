@@ -262,17 +262,29 @@ struct TileOf {
   __amdgpu_buffer_rsrc_t xbuf, wbuf, scbuf;
   uint32_t sc_off;
 
-  __device__ __forceinline__ explicit TileOf(const Fp8Product& p) {
-    const int tid = threadIdx.x;
-    lane = tid & 63;
-    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Tile `number` in the order of the launch.
+  __device__ __forceinline__ TileOf(const Fp8Product& p, int number) {
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lane = threadIdx.x & 63;
+    find(p, number);
+  }
+  // Another tile: with the lane's number found anew, so that nothing made from it is kept in between.
+  __device__ __forceinline__ TileOf(const Fp8Product& p, int number, int of_wave) {
+    wave = of_wave;
+    uint32_t zero;
+    asm volatile("s_mov_b32 %0, 0" : "=s"(zero));
+    lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+    find(p, number);
+  }
+  __device__ __forceinline__ void find(const Fp8Product& p, int number) {
+    const int tid = 64 * wave + lane;
     wm = wave / WN;
     wn = wave % WN;
     l16 = lane & 15;
     g = lane >> 4;
     // tiles in groups of p.group tiles of x, so that an XCD's share rows of both operands in its L2
     const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (int)((p.M + BM - 1) / BM);
-    const int bid = xcd_run((int)blockIdx.x, tiles_m * tiles_n);
+    const int bid = xcd_run(number, tiles_m * tiles_n);
     const int first = bid / (p.group * tiles_n) * p.group, gsize = min(tiles_m - first, p.group);
     const int in = bid % (p.group * tiles_n);
     m0 = (int64_t)(first + in % gsize) * BM;
@@ -374,6 +386,41 @@ struct TileOf {
     }
   }
 
+  // No rows at all: loads return zeros and fetch nothing.
+  __device__ __forceinline__ void clear(const Fp8Product& p) { xbuf = wbuf = scbuf = make_buf(p.x, 0); }
+
+  // bf16 rows in 16-byte stores through 2 KB of LDS a wave, 16 rows of 64 columns
+  // at a time: always kStores instructions a wave (rows and columns that are not
+  // there go past the buffer's end).
+  static constexpr int kStores = TM * WBN / 32;
+  __device__ __forceinline__ void store_through(const Fp8Product& p, u32x4* lds, const f32x4 (&acc)[TN][TM]) const {
+    static_assert(WBN % 64 == 0, "64 columns at a time");
+    const __amdgpu_buffer_rsrc_t ybuf = make_buf(reinterpret_cast<uint16_t*>(p.y) + m0 * p.y_stride + n0,
+                                                 (uint32_t)((rows - 1) * p.y_stride + wrows) * 2u);
+    uint32_t* const out = reinterpret_cast<uint32_t*>(lds + 128 * wave);
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int h = 0; h < WBN / 64; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 v = acc[4 * h + i][j];
+          *reinterpret_cast<u32x2*>(out + (8 * l16 + ((2 * i + (g >> 1)) ^ (l16 & 7))) * 4 + 2 * (g & 1)) =
+              u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int m = 8 * q + (lane >> 3), c = lane & 7;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(out + (8 * m + (c ^ (m & 7))) * 4);
+          const int row = wm * WBM + 16 * j + m, n = wn * WBN + 64 * h + 8 * c;
+          const uint32_t at = ((uint32_t)row * (uint32_t)p.y_stride + (uint32_t)n) * 2u;
+          __builtin_amdgcn_raw_buffer_store_b128(v, ybuf, row < rows && n < wrows ? at : kBufOOB, 0, kBufNT);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+  }
+
   template <int LDS>
   __device__ __forceinline__ void store(const Fp8Product& p, void* lds, const f32x4 (&acc)[TN][TM]) const {
     // A lane has, of a tile, one row of x and four rows of the weight.  bf16
@@ -410,6 +457,12 @@ struct TileOf {
       }
       return;
     }
+    store_each(p, acc);
+  }
+
+  // Rows straight from the registers.
+  __device__ __forceinline__ void store_each(const Fp8Product& p, const f32x4 (&acc)[TN][TM]) const {
+    const int nw = n0 + wn * WBN;
     const bool fours = !p.bf16 && (p.y_stride & 3) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
@@ -436,22 +489,30 @@ struct TileOf {
 
 // Large tiles: registers for one block's fragments of x and four of the weight's
 // only, so a step meets twice, once for each half of what the loads overwrite.
-// 4096 x 14336 x 4096 to bf16: 225 us, 2.14 PFLOP/s (256 x 256, 8 waves); it
-// waits for the fill of the L2s and, with the clock at its power limit, for the matrix
-// units.
-template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
-__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_tile_kernel(Fp8Product p) {
+// A step of 256 x 256 (8 waves) takes 1.64 us on the whole chip, 1.11 in one
+// workgroup alone (without the multiply-adds 9% less, without loads 12%, the matrix
+// instructions alone 0.85); with all of it the clock is at its power limit, 2.0 GHz.
+// STAY: a workgroup goes on to further tiles, whose first blocks are loaded in
+// the last steps of the one before, and stores while they are on their way (4096 x
+// 28672 x 4096 414 -> 402 us, 6000 x 8192 x 2048 102 -> 96, 8192 x 8192 x 8192 456 ->
+// 454).
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE, bool STAY>
+__global__ __launch_bounds__(WM * WN * 64)
+__attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_tile_kernel(Fp8Product p) {
   using Tile = TileOf<BM, BN, WM, WN>;
   constexpr int XD = Tile::XD, WD = Tile::WD, TM = Tile::TM, TN = Tile::TN, WBM = Tile::WBM, WBN = Tile::WBN;
   constexpr int LAST = 2, WB = 4;                    // rows of tiles behind a step's second barrier; fragments held
   struct Stages {
     u32x4 x[NS][BM * 8], w[NS][BN * 8];
     f32x4 scales[2][(Tile::XSW + 1) * 64], unused[64];  // of 4 blocks a row
+    u32x4 out[STAY ? 128 * WM * WN : 1];
   };
   __shared__ __attribute__((aligned(16))) Stages st;
 
-  const Tile t(p);
+  Tile t(p, (int)blockIdx.x), next = t;
   const int wave = t.wave, G = t.G;
+  const int steps = STAY ? (G + 1) & ~1 : G;  // (two of them use the two stages)
+  int flip = 0;                               // of the two places for scales
 
   // A wave's loads of the weight are half of the first halves of the WN waves'
   // rows, half of the second halves (and x's go by the same order where there
@@ -469,14 +530,15 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   // Load q of block b (the last one again past the end): 0 .. XD - 1 x, then
   // the first and the second half of the weight's.
   constexpr int L1 = XD + WD / 2, L2 = WD / 2;
-  const auto dma = [&](int stage, int b, int q) {
-    const uint32_t k = 128u * (uint32_t)min(b, G - 1);
-    if (q < XD) t.load_x(st.x[stage], x_at(q), x_off[q], k, p.K);
-    else buffer_to_lds16(t.wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
+  const auto column = [&](int b) { return 128u * (uint32_t)(STAY ? b : min(b, G - 1)); };
+  const auto dma = [&](const Tile& of, int stage, int b, int q) {
+    const uint32_t k = column(b);
+    if (q < XD) of.load_x(st.x[stage], x_at(q), x_off[q], k, p.K);
+    else buffer_to_lds16(of.wbuf, st.w[stage] + 8 * w_at(q - XD), w_off[q - XD], k);
   };
   static_assert(NS <= 5, "a block's scales are read before those of the block 8 later come");
-  const auto dma_scales = [&](int b) {
-    t.load_scales(st.scales[(b >> 2) & 1], st.unused, b, 128u * (uint32_t)min(b, G - 1));
+  const auto dma_scales = [&](const Tile& of, int b, int f) {
+    of.load_scales(st.scales[((b >> 2) + f) & 1], st.unused, b, column(b));
   };
 
   // Fragments: chunks g and g + 4 of a row, the same columns of both operands.
@@ -485,17 +547,20 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   const int x0 = x_row + c0, x1 = x_row + c1, w0 = w_row + c0, w1 = w_row + c1;
   Fragment8<WIDE> xf[TM], wf[WB];
   float s[TM], xsc[TM], wsc, s_last = 0.0f;
-  bool odd = false;
+  bool odd = false, odd_next = false;
   const auto load_x = [&](int stage, int j, int h) { xf[j].q[h] = st.x[stage][(h ? x1 : x0) + 128 * j]; };
   const auto load_w = [&](int stage, int i, int h) { wf[i % WB].q[h] = st.w[stage][(h ? w1 : w0) + 128 * i]; };
-  const auto load_scales = [&](int b) { t.read_scales(st.scales[(b >> 2) & 1], b, xsc, wsc); };
-  const auto factor = [&](int j) { Tile::factor(xsc[j], wsc, s[j], odd); };
+  const auto load_scales = [&](int b, int f) { t.read_scales(st.scales[((b >> 2) + f) & 1], b, xsc, wsc); };
+  const auto factor = [&](int j, bool& o) { Tile::factor(xsc[j], wsc, s[j], o); };
 
   f32x4 acc[TN][TM];
+  const auto clear = [&] {
 #pragma unroll
-  for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-    for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  };
+  clear();
 
   const auto multiply = [&](int i, int j) { return wf[i % WB].times(xf[j]); };
   // Tile q of a step: rows 0 .. TN - LAST - 1, then the columns of the last
@@ -536,26 +601,40 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   constexpr int SLACK = L1 + 1 + L2;  // loads of a block, one for scales among them
   static_assert((NS - 1) * SLACK + L2 <= 63, "the counter of loads in flight");
   // (The matrix instruction goes first in a tile, so that it is issued right behind a meet.)
-  const auto step = [&](int b, int cur) {
+  // STAY: in a tile's first step both meets, in its second one the first, have
+  // the stores of the tile before among the operations that may be outstanding
+  // (STORED; in the first tile everything the meets wait for has landed).  The last
+  // two steps (BEFORE: so many behind them) load the next tile's first blocks.
+  const auto step = [&](int b, int cur, auto stored, auto before) {
+    constexpr int STORED = decltype(stored)::value, BEFORE = decltype(before)::value;
+    constexpr int W0 = (NS - 1) * SLACK + (STORED > 0 ? Tile::kStores : 0);
+    constexpr int W1 = (NS - 1) * SLACK + (STORED > 1 ? Tile::kStores : 0);
+    static_assert(W0 <= 63, "the counter of operations in flight");
+    constexpr bool ENDS = STAY && BEFORE < NS;
     const int nxt = (cur + 1) % NS;
+    const Tile& of = ENDS ? next : t;
+    const int to = ENDS ? NS - 1 - BEFORE : b + NS, f = flip + (ENDS ? (steps + 3) >> 2 : 0);
 #pragma unroll
     for (int q = 0; q < T0; ++q) {
       const int i = q / TM, c = q % TM;
-      if (q == A * TM) meet(std::integral_constant<int, (NS - 1) * SLACK>{});
+      if (q == A * TM) meet(std::integral_constant<int, W0>{});
       multiply_tile(q);
       if (c < 2) load_w(cur, i + 2, c);
 #pragma unroll
       for (int l = 0; l < L1; ++l)
-        if (q == A * TM + l * (T0 - A * TM) / L1) dma(cur, b + NS, l);
-      if (q == T0 - 1) dma_scales(b + NS);
+        if (q == A * TM + l * (T0 - A * TM) / L1) dma(of, cur, to, l);
+      if (q == T0 - 1) dma_scales(of, to, f);
       add_tile(q);
     }
-    meet(std::integral_constant<int, (NS - 1) * SLACK>{});
+    meet(std::integral_constant<int, W1>{});
+    // the next block's factors; of the one that only fills a pair of steps they do not count
+    bool& o = STAY && BEFORE == 0 ? odd_next : odd;
+    const bool kept = odd;
 #pragma unroll
     for (int q = T0; q < TILES; ++q) {
       const int c = (q - T0) / LAST, in_c = (q - T0) % LAST;
       multiply_tile(q);
-      if (q == T0) load_scales(b + 1);
+      if (q == T0) load_scales(STAY && BEFORE == 0 ? 0 : b + 1, STAY && BEFORE == 0 ? f : flip);
       if (q - T0 < 4) load_w(nxt, (q - T0) / 2, (q - T0) % 2);
       if (in_c == LAST - 1) {
         load_x(nxt, c, 0);
@@ -563,62 +642,105 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
       }
 #pragma unroll
       for (int l = 0; l < L2; ++l)
-        if (q == T0 + l * (TILES - T0) / L2) dma(cur, b + NS, L1 + l);
+        if (q == T0 + l * (TILES - T0) / L2) dma(of, cur, to, L1 + l);
       add_tile(q);
       // a column's factor, once its last sums have been added
       if (q == T0 + 2) {
         s_last = s[TM - 1];
-        factor(TM - 1);
+        factor(TM - 1, o);
       }
-      if (in_c == LAST - 1 && c >= 2) factor(c - 2);
+      if (in_c == LAST - 1 && c >= 2) factor(c - 2, o);
     }
-    factor(TM - 2);
+    factor(TM - 2, o);
+    if (STAY && BEFORE == 1 && steps != G) odd = kept;
   };
   static_assert(TM >= 2, "a tile a fragment's load");
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, NS> far{};
 
 #pragma unroll
   for (int b = 0; b < NS; ++b) {
 #pragma unroll
-    for (int q = 0; q < L1; ++q) dma(b, b, q);
-    dma_scales(b);
+    for (int q = 0; q < L1; ++q) dma(t, b, b, q);
+    dma_scales(t, b, 0);
 #pragma unroll
-    for (int q = L1; q < L1 + L2; ++q) dma(b, b, q);
+    for (int q = L1; q < L1 + L2; ++q) dma(t, b, b, q);
   }
-  meet(std::integral_constant<int, (NS - 1) * SLACK + L2>{});
-  load_scales(0);
+  if constexpr (STAY) meet(none);
+  else meet(std::integral_constant<int, (NS - 1) * SLACK + L2>{});
+  load_scales(0, 0);
+  const auto load_first = [&] {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int j = 0; j < TM; ++j) load_x(0, j, h);
-    load_w(0, 0, h);
-    load_w(0, 1, h);
-  }
+      for (int j = 0; j < TM; ++j) load_x(0, j, h);
+      load_w(0, 0, h);
+      load_w(0, 1, h);
+    }
+  };
+  load_first();
 #pragma unroll
-  for (int j = 0; j < TM; ++j) factor(j);
-  int b = 0;
-  for (; b + NS <= G; b += NS) {
-    step(b, 0);
-    step(b + 1, 1);
-    if constexpr (NS > 2) step(b + 2, 2);
-    if constexpr (NS > 3) step(b + 3, 3);
-    if constexpr (NS > 4) step(b + 4, 4);
-  }
-  if (b < G) step(b, 0);
-  if constexpr (NS > 2) {
-    if (b + 1 < G) step(b + 1, 1);
-  }
-  if constexpr (NS > 3) {
-    if (b + 2 < G) step(b + 2, 2);
-  }
-  if constexpr (NS > 4) {
-    if (b + 3 < G) step(b + 3, 3);
-  }
+  for (int j = 0; j < TM; ++j) factor(j, odd);
+  if constexpr (STAY) {
+    static_assert(NS == 2, "steps in pairs");
+    const int tiles = (int)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+    for (int number = (int)blockIdx.x;; number += (int)gridDim.x) {
+      const bool more = number + (int)gridDim.x < tiles;
+      step(0, 0, std::integral_constant<int, 2>{}, far);
+      step(1, 1, std::integral_constant<int, 1>{}, far);
+#pragma unroll 1
+      for (int b = 2; b < steps - 2; b += 2) {
+        step(b, 0, none, far);
+        step(b + 1, 1, none, far);
+      }
+      next = Tile(p, more ? number + (int)gridDim.x : number, wave);
+      if (!more) next.clear(p);
+      step(steps - 2, 0, none, std::integral_constant<int, 1>{});
+      step(steps - 1, 1, none, std::integral_constant<int, 0>{});
 #pragma unroll
-  for (int q = TILES - LAG; q < TILES; ++q) add(q, s_last);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
-
-  if (__ballot(odd)) t.template other_blocks<WIDE>(p, acc);
-  t.template store<(int)sizeof(st)>(p, &st, acc);
+      for (int q = TILES - LAG; q < TILES; ++q) {
+        add(q, s_last);
+        d[q % 4] = f32x4{0, 0, 0, 0};
+      }
+      const Tile done(p, number, wave);
+      if (__ballot(odd)) {
+        done.template other_blocks<WIDE>(p, acc);
+        load_first();  // (so that they need not be kept meanwhile)
+      }
+      if ((p.y_stride & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0) {
+        done.store_through(p, st.out, acc);
+      } else {
+        done.store_each(p, acc);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+      }
+      if (!more) break;
+      t.xbuf = next.xbuf;
+      t.wbuf = next.wbuf;
+      t.scbuf = next.scbuf;
+      t.sc_off = next.sc_off;
+      flip += (steps + 3) >> 2;
+      odd = odd_next;
+      odd_next = false;
+      clear();
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
+  } else {
+    int b = 0;
+    for (; b + NS <= G; b += NS) {
+      step(b, 0, none, far);
+      step(b + 1, 1, none, far);
+      if constexpr (NS > 2) step(b + 2, 2, none, far);
+    }
+    if (b < G) step(b, 0, none, far);
+    if constexpr (NS > 2) {
+      if (b + 1 < G) step(b + 1, 1, none, far);
+    }
+#pragma unroll
+    for (int q = TILES - LAG; q < TILES; ++q) add(q, s_last);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // nothing in flight into LDS when the workgroup ends
+    if (__ballot(odd)) t.template other_blocks<WIDE>(p, acc);
+    t.template store<(int)sizeof(st)>(p, &st, acc);
+  }
 }
 
 // Small tiles: the fragments of two blocks fit the registers, so the next
@@ -626,7 +748,8 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
 // 333 x 5000 x 4112 with 64 x 128 tiles, the kernel above and this one: 27.2 and
 // 22.9 us to bf16, 33.7 and 27.8 to fp32.
 template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
-__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_pipe_kernel(Fp8Product p) {
+__global__ __launch_bounds__(WM * WN * 64)
+__attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_pipe_kernel(Fp8Product p) {
   using Tile = TileOf<BM, BN, WM, WN>;
   constexpr int XD = Tile::XD, WD = Tile::WD, TM = Tile::TM, TN = Tile::TN, WBM = Tile::WBM, WBN = Tile::WBN;
   struct Stages {
@@ -635,7 +758,7 @@ __global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(WM
   };
   __shared__ __attribute__((aligned(16))) Stages st;
 
-  const Tile t(p);
+  const Tile t(p, (int)blockIdx.x);
   const int wave = t.wave, G = t.G;
 
   const auto x_at = [&](int j) { return 8 * (wave * XD + j); };
@@ -821,11 +944,18 @@ hipError_t launch_pipe(const Fp8Product& p, hipStream_t stream) {
   });
 }
 
-template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
+template <int BM, int BN, int WM, int WN, int NS, bool WIDE, bool STAY>
 hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
-  return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 grid) {
-    hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, NS, WIDE>), grid, dim3(64 * WM * WN), 0, stream, q);
+  return launch_tiles(p, BM, BN, [=](const Fp8Product& q, dim3 tiles) {
+    const dim3 grid(STAY ? std::min(tiles.x, 256u) : tiles.x);
+    hipLaunchKernelGGL((fp8_gemm_tile_kernel<BM, BN, WM, WN, NS, WIDE, STAY>), grid, dim3(64 * WM * WN), 0, stream, q);
   });
+}
+
+// 256 x 256: at least two pairs of steps, and rows of y that 32-bit offsets reach.
+hipError_t launch_256(const Fp8Product& p, hipStream_t stream) {
+  if (p.K > 256 && p.y_stride <= 1 << 21) return launch_tile<256, 256, 4, 2, 2, false, true>(p, stream);
+  return launch_tile<128, 256, 2, 4, 3, false, false>(p, stream);
 }
 
 // Kernels of many rows, and the time of a step (a block of 128 columns of all
@@ -851,12 +981,12 @@ struct TileKernel {
 const TileKernel kTiles16[] = {{32, 64, 0.30, 0.46, launch_pipe<32, 64, 1, 2, 5, false>},
                                {64, 64, 0.33, 0.64, launch_pipe<64, 64, 2, 2, 4, false>},
                                {64, 128, 0.50, 0.88, launch_pipe<64, 128, 2, 2, 3, false>},
-                               {128, 128, 0.66, 1.15, launch_tile<128, 128, 2, 2, 2, false>},
-                               {128, 256, 1.07, 0.0, launch_tile<128, 256, 2, 4, 3, false>},
-                               {256, 256, 1.80, 0.0, launch_tile<256, 256, 4, 2, 2, false>}};
+                               {128, 128, 0.66, 1.15, launch_tile<128, 128, 2, 2, 2, false, false>},
+                               {128, 256, 1.07, 0.0, launch_tile<128, 256, 2, 4, 3, false, false>},
+                               {256, 256, 1.80, 0.0, launch_256}};
 const TileKernel kTiles32[] = {{64, 64, 0.47, 0.78, launch_pipe<64, 64, 2, 2, 4, true>},
                                {64, 128, 0.73, 1.30, launch_pipe<64, 128, 2, 2, 3, true>},
-                               {128, 128, 1.15, 2.00, launch_tile<128, 128, 2, 2, 2, true>}};
+                               {128, 128, 1.15, 2.00, launch_tile<128, 128, 2, 2, 2, true, false>}};
 
 // The kernel of the least estimated time, or two: whole rounds of one with one
 // workgroup a CU for the first columns or rows and the best for the rest, where

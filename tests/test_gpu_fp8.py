@@ -310,9 +310,10 @@ def test_gemm_scales_at_the_ends_of_fp32(M):
 
 
 # A size for each of the launcher's kernels (16, 32, 64, 128 and 256 rows of x a
-# workgroup, with N that allows 16-byte stores and that does not).
+# workgroup, with N that allows 16-byte stores and that does not), several tiles a
+# workgroup, and two launches.
 TILES = [(7, 9001), (9, 8904), (33, 4144), (131, 2137), (390, 1411), (40, 8400), (270, 6005), (700, 2056), (201, 8301),
-         (513, 5016), (390, 9349), (1100, 6008), (1156, 6805), (900, 8752)]
+         (513, 5016), (390, 9349), (1100, 6008), (1156, 6805), (900, 8752), (3300, 9001), (3300, 9000), (2000, 16600)]
 
 
 @pytest.mark.parametrize("M,N", TILES)
