@@ -7,7 +7,7 @@
 // where there are many tokens (65536 tokens of 8 heads of 128, bf16: written
 // in 91 us, 4.5 TB/s, read in 87, 4.7), and below about a thousand the launch
 // and the three reads that follow each other (cu, page number, codes): 4.5 us.
-// Found once a workgroup the places cost 87 us, found by every thread 137.
+// (Every thread finding its own place and moving one vector: 137 us.)
 #include "device_common.hpp"
 #include "encode8.hpp"
 #include "fp8_kernels.hpp"
