@@ -357,6 +357,40 @@ def test_gemm_tiles_with_scales_at_the_ends_of_fp32(M, N):
         assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outputs"
 
 
+@pytest.mark.parametrize("M,N", [(5, 264), (300, 264), (700, 2056), (513, 5016), (3300, 9000)])
+def test_gemm_output_aligned_to_4_bytes(M, N):
+    K = 400
+    x, w = operand(M, K, 37, "whole"), operand(N, K, 38, "whole")
+    xs, ws = scales(M, 4, seed=39, power=True), scales(-(-N // 128), 4, seed=40, power=True)
+    want = fp8.gemm(x, xs, w, ws, out_dtype=FL)
+    for dtype, at in ((BF, 2), (FL, 1), (FL, 2)):
+        whole = torch.full((M * N + 64,), 5.0, dtype=dtype, device=DEV)
+        fp8.gemm(x, xs, w, ws, out=whole[at:at + M * N].view(M, N))
+        assert torch.equal(whole[at:at + M * N].view(M, N), want.to(dtype))
+        assert bool((whole[:at] == 5.0).all()) and bool((whole[at + M * N:] == 5.0).all())
+
+
+def test_gemm_many_at_once():
+    """Large products on four streams at a time, which share nothing."""
+    sizes = [(1300, 6000, 784), (900, 8752, 528), (3300, 9000, 400), (2000, 16600, 1040)]
+    ops = []
+    for i, (M, N, K) in enumerate(sizes):
+        G = -(-K // 128)
+        ops.append((operand(M, K, 50 + i, "plain"), scales(M, G, seed=60 + i), operand(N, K, 70 + i, "plain"),
+                    scales(-(-N // 128), G, seed=80 + i)))
+    want = [fp8.gemm(*o) for o in ops]
+    streams = [torch.cuda.Stream() for _ in ops]
+    got = [[] for _ in ops]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o, g in zip(streams, ops, got):
+            with torch.cuda.stream(s):
+                g.append(fp8.gemm(*o))
+    torch.cuda.synchronize()
+    for y, g in zip(want, got):
+        assert all(torch.equal(y, a) for a in g)
+
+
 def test_gemm_longest_rows():
     """K = 2^22, the most the call takes: sums of 2^22 products in every tile kernel."""
     K = 1 << 22
