@@ -107,7 +107,10 @@ def gemm(x, x_scales, codes, scales, out_dtype=torch.bfloat16, out=None):
     """y = (x_scales x) (scales codes)^T, [M, N] of bf16 or fp32.
 
     x float8_e4m3fn [M, K] with x_scales float32 [M, ceil(K / 128)]; codes and
-    scales as quantize returns them for a [N, K] weight.  Any M."""
+    scales as quantize returns them for a [N, K] weight.  Any M.  Sums are
+    fp32's, but the FP8 matrix instruction, which takes the bf16 products of many
+    rows, cuts each 8 columns' products off 13 bits below their largest
+    (include/fp8.h has the bound); out_dtype=torch.float32 never does."""
     M, K = _i4._matrix(x, "x")
     N, Kw = _i4._matrix(codes, "codes")
     if K != Kw:

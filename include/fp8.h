@@ -81,11 +81,13 @@ int fp8_quantize_act(const void* x, int64_t x_stride, const void* gate, int64_t 
  *   y [M, N] of y_dtype (NVFP4_BF16 or NVFP4_F32), contiguous
  * Products of codes are summed within a block, and blocks among each other, in
  * fp32 in an order that M, N, K and y_dtype fix: the same call gives the same
- * bits. An fp32 y, and a bf16 y of few rows before its rounding, is off by at
- * most (K + 4) 2^-24 of the sum of all terms' magnitudes |x^ w^|. The sums
- * behind a bf16 y of more rows (M > 16 and ceil(M / 32) ceil(N / 16) > 512) also
- * lose up to 7 2^-13 of the largest term of each 8 columns, what the FP8 matrix
- * instruction cuts off.
+ * bits. An fp32 y of any size, and a bf16 y of few rows before its rounding, is
+ * off by at most (K + 4) 2^-24 of the sum of all terms' magnitudes |x^ w^|. The
+ * sums behind a bf16 y of more rows (M > 16 and ceil(M / 32) ceil(N / 16) > 512)
+ * also lose up to 7 2^-13 of the largest term of each 8 columns, what the FP8
+ * matrix instruction cuts off: less than bf16's rounding of a typical result, but
+ * not of one whose terms cancel, and a row's results depend in this on how many
+ * rows the call has. Where that matters, ask for an fp32 y.
  * xs ws may leave fp32's range as long as xs ws x w does not.
  * K % 16 != 0: NVFP4_ERR_SHAPE; K == 0, K > 2^22, N > 2^26 or M > 2^31:
  * NVFP4_ERR_UNSUPPORTED. x and w 16-byte aligned, scales and y 4.
