@@ -45,16 +45,19 @@ constexpr int kWaitLgkm0 = 15 | (3 << 14) | (7 << 4);
 // NaN, infinity, subnormal or zero.
 __device__ __forceinline__ bool not_normal(float v) { return __builtin_amdgcn_classf(v, 0x2F7); }
 
-// acc += xs ws d.  The product of the scales is used where it is a normal number
-// in all lanes; elsewhere it could leave fp32's range although xs ws d does not.
+// acc += xs ws d.  The product of the scales is used where it is a normal number;
+// elsewhere it could leave fp32's range although xs ws d does not.  (Lane by lane:
+// a row of x has the same sums whatever the scales of the others are.)
 __device__ __forceinline__ void add_scaled(f32x4 d, float ws, float xs, f32x4& acc) {
   const float s = ws * xs;
-  if (__ballot(not_normal(s)) == 0) {
+  const bool odd = not_normal(s);
+  if (__ballot(odd) == 0) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d[r], s, acc[r]);
   } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] += (float)((double)d[r] * ((double)ws * (double)xs));
+    for (int r = 0; r < 4; ++r)
+      acc[r] = odd ? acc[r] + (float)((double)d[r] * ((double)ws * (double)xs)) : __builtin_fmaf(d[r], s, acc[r]);
   }
 }
 
@@ -150,7 +153,9 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
         buffer_to_lds16(xbuf, st[s].x[t] + 64 * h, x_ok ? row_off + (uint32_t)(16 * t + 8 * h) * (uint32_t)p.K + c : kBufOOB, 0);
     }
   };
-  // scales of a run's blocks (past a row's end whatever the next one holds, or 0: those blocks' sums are 0)
+  // scales of a run's blocks: a load of x's takes what the next row holds behind a
+  // row's last, and 1 stands for that in the blocks past the end (their sums are 0,
+  // and 0 times a scale that is no number would not be)
   static_assert(P == 2 || P == 4, "one load of scales");
   uint32_t s_off[MT];
 #pragma unroll
@@ -194,7 +199,7 @@ __global__ __launch_bounds__(64 * W) void fp8_gemm_rows_kernel(Fp8Product p) {
         Fragment wb;
         wb.load(st[s].w[t], at0, at1);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) add_scaled(wb.times(xb[i]), wsc[0][s], xs[0][i][s], acc[i][t]);
+        for (int i = 0; i < MT; ++i) add_scaled(wb.times(xb[i]), wsc[0][s], b + s < G ? xs[0][i][s] : 1.0f, acc[i][t]);
       }
       // the stage has been read
       __builtin_amdgcn_s_waitcnt(kWaitLgkm0);

@@ -89,6 +89,8 @@ int fp8_quantize_act(const void* x, int64_t x_stride, const void* gate, int64_t 
  * not of one whose terms cancel, and a row's results depend in this on how many
  * rows the call has. Where that matters, ask for an fp32 y.
  * xs ws may leave fp32's range as long as xs ws x w does not.
+ * A row of x whose codes or scales are no numbers (behind a padded batch, say)
+ * reaches its own row of y only; in a weight they are a caller error.
  * K % 16 != 0: NVFP4_ERR_SHAPE; K == 0, K > 2^22, N > 2^26 or M > 2^31:
  * NVFP4_ERR_UNSUPPORTED. x and w 16-byte aligned, scales and y 4.
  */

@@ -53,3 +53,31 @@ def test_product_bound(M, N, K, kind):
     tau = tau * (1 + HALF_BF16) + HALF_BF16 * ystar.abs()
     err = (fp8.gemm(x, xs, w, ws).double() - ystar).abs()
     assert bool((err <= tau).all()), f"bf16: worst {float((err / tau).max())} of the bound"
+
+
+# every rows kernel, and kernels of many rows; G = 5, 9 and 33: the last blocks of a row are no whole run of any kernel's
+NEIGHBOURS = [(2, 64, 640), (15, 300, 1040), (16, 8300, 656), (16, 4096, 4112), (40, 64, 640), (130, 512, 1040), (33, 5000, 640),
+              (70, 5000, 1040), (300, 264, 640), (390, 1411, 1040), (700, 2056, 656), (513, 5016, 1040), (3300, 9000, 400)]
+
+
+@pytest.mark.parametrize("M,N,K", NEIGHBOURS)
+@pytest.mark.parametrize("bad", ["scales", "codes", "scale_range"])
+def test_rows_do_not_meet(M, N, K, bad):
+    """Rows of x whose scales or codes are no numbers (rows behind a padded batch,
+    say), or whose scales are below fp32's normal numbers, leave the results of all
+    others as they are, bit for bit."""
+    print(f"[case] gemm neighbours {bad} {M}x{N}x{K}", flush=True)
+    x, w = operand(M, K, 111, "plain"), operand(N, K, 112, "plain")
+    G = -(-K // 128)
+    xs, ws = scales(M, G, seed=113), scales(-(-N // 128), G, seed=114)
+    x2, xs2 = x.view(torch.uint8).clone(), xs.clone()
+    if bad == "codes":
+        x2[1::2] = 0x7F
+    else:
+        xs2[1::2] = 1e-41 if bad == "scale_range" else torch.tensor([float("nan"), float("inf")], device=DEV).repeat(G)[:G]
+    for dtype in (BF, FL):
+        want = fp8.gemm(x, xs, w, ws, out_dtype=dtype)
+        got = fp8.gemm(x2.view(x.dtype), xs2, w, ws, out_dtype=dtype)
+        assert torch.equal(got[::2], want[::2])
+        if bad != "scale_range":
+            assert not bool(torch.isfinite(got[1::2]).any())
