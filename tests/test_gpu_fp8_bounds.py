@@ -81,3 +81,33 @@ def test_rows_do_not_meet(M, N, K, bad):
         assert torch.equal(got[::2], want[::2])
         if bad != "scale_range":
             assert not bool(torch.isfinite(got[1::2]).any())
+
+
+def fastest(calls, rounds=7):
+    """The shortest time of each call among others of its kind (us), taken in turn."""
+    best = [float("inf")] * len(calls)
+    for r in range(rounds):
+        for i, call in enumerate(calls):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(20):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            if r:
+                best[i] = min(best[i], a.elapsed_time(b) / 20 * 1e3)
+    return best
+
+
+def test_time_goes_by_the_blocks():
+    """86 and 33 blocks of columns take no longer than 88 and 36 do: no block is
+    taken again because of scales that are not there (that cost two fifths)."""
+    for M, N, K, longer in ((1000, 4096, 11008, 11264), (1000, 4096, 4224, 4608)):
+        calls = []
+        for k in (K, longer):
+            x, w, G = operand(M, k, 121, "plain"), operand(N, k, 122, "plain"), k // 128
+            ops = x, scales(M, G, seed=123), w, scales(N // 128, G, seed=124)
+            calls.append(lambda ops=ops: fp8.gemm(*ops))
+        t = fastest(calls)
+        print(f"[case] {M}x{N}: {K} {t[0]:.1f} us, {longer} {t[1]:.1f} us", flush=True)
+        assert t[0] < 1.15 * t[1]
