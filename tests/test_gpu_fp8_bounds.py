@@ -111,3 +111,32 @@ def test_time_goes_by_the_blocks():
         t = fastest(calls)
         print(f"[case] {M}x{N}: {K} {t[0]:.1f} us, {longer} {t[1]:.1f} us", flush=True)
         assert t[0] < 1.15 * t[1]
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(300, 4096, 4096, BF), (1000, 4096, 4096, BF), (1000, 4096, 4096, FL), (4096, 4096, 2048, BF)])
+def test_scales_of_zero(M, N, K, dtype):
+    """Rows, and blocks of the weight, with scales of 0 (a padded batch in buffers of
+    zeros) give zeros, the others what they gave, and none of it takes longer: no
+    block is taken again for a factor of 0 (one such row made a call 4 times as long)."""
+    x, w = operand(M, K, 131, "plain"), operand(N, K, 132, "plain")
+    G = K // 128
+    xs, ws = scales(M, G, seed=133), scales(N // 128, G, seed=134)
+    zx, zw = xs.clone(), ws.clone()
+    zx[M // 2:] = 0
+    zx[0, 3] = 0
+    zw[1], zw[:, 5] = 0, 0
+    one = xs.clone()
+    one[M - 1] = 0
+    want = fp8.gemm(x, xs, w, ws, out_dtype=dtype)
+    got = fp8.gemm(x, one, w, ws, out_dtype=dtype)
+    assert torch.equal(got[:-1], want[:-1]) and not bool(got[-1].any())
+    got = fp8.gemm(x, zx, w, zw, out_dtype=dtype)
+    assert not bool(got[M // 2:].any()) and not bool(got[:, 128:256].any())
+    rest = ws.clone()
+    rest[:, 5] = 0
+    part = fp8.gemm(x, xs, w, rest, out_dtype=dtype)
+    assert torch.equal(got[1:M // 2, 256:], part[1:M // 2, 256:])
+    t = fastest([lambda: fp8.gemm(x, xs, w, ws, out_dtype=dtype), lambda: fp8.gemm(x, one, w, ws, out_dtype=dtype),
+                 lambda: fp8.gemm(x, zx, w, zw, out_dtype=dtype)])
+    print(f"[case] zero scales {M}x{N}x{K} {dtype}: {t[0]:.1f}, one row {t[1]:.1f}, many {t[2]:.1f} us", flush=True)
+    assert max(t[1:]) < 1.3 * t[0]
