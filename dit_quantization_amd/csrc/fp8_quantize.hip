@@ -82,7 +82,7 @@ hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t stride, int64_t
 // ---- activations.  A row is cut into slots of 16 columns, filled up to whole
 // groups, and slots go to threads in order, so that a group is 2, 4 or 8
 // neighbouring lanes.  4096 x 14336 bf16 to E4M3: 36 us, 4.9 TB/s; SiLU(gate) x
-// 68 us, 4.4 TB/s: memory, and fp64 arithmetic (a table's read, a product and a
+// 60 us, 4.9 TB/s: memory, and fp64 arithmetic (a table's read, a product and a
 // quotient a value) that would take half as long alone.
 
 // g / (1 + exp(-g)) to within 2^-45 of itself: exp(-g) = 2^n exp(r), |r| <= ln 2
@@ -107,8 +107,10 @@ __device__ __forceinline__ double silu64(float g) {
 
 // The same of a bf16 gate from a table: of both signs and all magnitudes from
 // 2^-16 up to 2^8, computed when this file is compiled (within 2^-48: ln 2 in two
-// parts, 17 terms of the series).
+// parts, 17 terms of the series).  Below it g / 2 + g^2 / 4 is within 2^-52, above
+// it g is, and under -2^8 a product with any x is below fp32's range.
 constexpr uint32_t kTableFirst = (127 - 16) << 7, kTableSize = 24 << 7;
+constexpr uint32_t kTableStride = kTableSize + 2;  // in LDS: behind the entries of a sign, that of a 0
 struct SiluTable {
   double v[2 * kTableSize];
   constexpr SiluTable() : v() {
@@ -129,8 +131,12 @@ __device__ constexpr SiluTable kSilu{};
 __device__ __forceinline__ void fill_table(double* table) {
   static_assert(kTableSize % 512 == 0, "two entries a thread at a time");
 #pragma unroll
-  for (uint32_t i = 0; i < 2 * kTableSize; i += 2 * 512)
-    *reinterpret_cast<u32x4*>(table + i + 2 * threadIdx.x) = *reinterpret_cast<const u32x4*>(kSilu.v + i + 2 * threadIdx.x);
+  for (uint32_t i = 0; i < 2 * kTableSize; i += 2 * 512) {
+    const uint32_t at = i + 2 * threadIdx.x;
+    *reinterpret_cast<u32x4*>(table + at + (at >= kTableSize ? kTableStride - kTableSize : 0)) =
+        *reinterpret_cast<const u32x4*>(kSilu.v + at);
+  }
+  if (threadIdx.x < 2) table[kTableSize + threadIdx.x * kTableStride] = threadIdx.x ? -0.0 : 0.0;
   __syncthreads();
 }
 
@@ -144,13 +150,15 @@ __device__ __forceinline__ T group_all(T v, int L, F f) {
 }
 
 // TABLE (bf16 gates): a grid of as many workgroups as fit at once, each with a
-// copy of the table in LDS.  For 8 million values and more: an exponential is 24
-// of 47 vector instructions a value (4096 x 14336 68 against 98 us; 512 x 14336
-// 15.0 against 14.2, where copying the table takes longer than it saves).
+// copy of the table in LDS.  For 2 million values and more: an exponential is 24
+// of 47 vector instructions a value (4096 x 14336 60 against 88 us, 512 x 14336 10.8
+// against 12.3, 128 x 14336 4.9 against 5.0).  Gates of 0 are an entry of it; others
+// outside take some 15 instructions each, in the lanes that have them (gates of spread 2, 0.02, 0, 2000:
+// 60, 64, 60, 75 us; one after the other, read again, with an exponential: 67, 137, 238, 240).
 template <bool BF, bool SILU, bool TABLE>
 __global__ __launch_bounds__(TABLE ? 512 : 256) void fp8_quantize_act_kernel(ActArgs a, uint32_t slots, uint32_t per,
                                                                               uint32_t all, double q, double inv_q) {
-  __shared__ __attribute__((aligned(16))) double table[TABLE ? 2 * kTableSize : 1];
+  __shared__ __attribute__((aligned(16))) double table[TABLE ? 2 * kTableStride : 1];
   if (TABLE) fill_table(table);
   const int L = a.group / 16;
   // (rounds of whole workgroups, so that all lanes of a group are there)
@@ -184,19 +192,21 @@ __global__ __launch_bounds__(TABLE ? 512 : 256) void fp8_quantize_act_kernel(Act
       if (TABLE) {
         const uint32_t w = g[j / 8].a[0][j % 8 / 2], bits = j & 1 ? w >> 16 : w & 0xFFFFu;
         const uint32_t entry = (bits & 0x7FFFu) - kTableFirst;
-        outside |= entry >= kTableSize;
-        y[j] *= table[min(entry, kTableSize - 1) + (bits >> 15) * kTableSize];
+        outside |= entry >= kTableSize && entry != 0u - kTableFirst;  // (not a gate of 0)
+        y[j] *= table[min(entry, kTableSize) + (bits >> 15) * kTableStride];
       }
     }
-    if (TABLE && live && outside) {  // a lane with a zero or a gate beyond the table's range
-#pragma unroll 1
-      for (int j = 0; j < 16; ++j) {
-        // (a loop, so that this path takes no registers: values are read again)
-        const float gate = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(a.gate)[r * a.gate_stride + c + j]);
-        const float of = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(a.x)[r * a.x_stride + c + j]);
-        const double v = silu64(gate) * (double)of;
+    if (TABLE && outside) {  // a lane with a gate beyond the table's range, few of them
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] = k == j ? v : y[k];
+      for (int j = 0; j < 16; ++j) {
+        // (from the vectors as they came: kept as fp64 they would take the registers of a workgroup a CU)
+        const uint32_t xw = fresh(x[j / 8].a[0][j % 8 / 2]), gw = fresh(g[j / 8].a[0][j % 8 / 2]);
+        const float f = __uint_as_float(j & 1 ? gw & 0xFFFF0000u : gw << 16);
+        if (fabsf(f) < 0x1p-16f || fabsf(f) >= 0x1p8f) {
+          const double gate = (double)f, of = (double)__uint_as_float(j & 1 ? xw & 0xFFFF0000u : xw << 16);
+          const double half = fabsf(f) < 1.0f ? __builtin_fma(gate, 0.25, 0.5) : f > 0.0f ? 1.0 : 0.0;
+          y[j] = of * (gate * half);
+        }
       }
     }
 #pragma unroll
@@ -237,7 +247,7 @@ hipError_t launch_fp8_quantize_act(const ActArgs& all, hipStream_t stream) {
 #define ACT_CASE(BF, SILU, TABLE, GRID)                                                                        \
   hipLaunchKernelGGL((fp8_quantize_act_kernel<BF, SILU, TABLE>), dim3(GRID), dim3(TABLE ? 512 : 256), 0, stream, a, \
                      slots, per, n, q, 1.0 / q)
-    if (a.gate && a.bf16 && n >= (1u << 19)) ACT_CASE(true, true, true, 768);
+    if (a.gate && a.bf16 && n >= (1u << 17)) ACT_CASE(true, true, true, 768);
     else if (a.gate && a.bf16) ACT_CASE(true, true, false, (n + 255) / 256);
     else if (a.gate) ACT_CASE(false, true, false, (n + 255) / 256);
     else if (a.bf16) ACT_CASE(true, false, false, (n + 255) / 256);

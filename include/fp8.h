@@ -58,7 +58,9 @@ int fp8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int
  *   y[r, c] = x[r, c], or with a gate x[r, c] g / (1 + exp(-g)), g = gate[r, c]
  *   (never rounded to 16 or 32 bits: a code or scale is decided by the
  *   definition above, short of values within 2^-44 of a border between two
- *   codes, relative, which fp64 cannot tell from it)
+ *   codes, relative, which fp64 cannot tell from it; of these two calls of
+ *   different sizes may take the one and the other, since large ones have
+ *   SiLU from a table)
  *   x      [rows, cols] of x_dtype (NVFP4_F32 or NVFP4_BF16), rows x_stride
  *          elements apart; gate the same, rows gate_stride apart, or NULL
  *          (the two halves of one [rows, 2 cols] product, say)
