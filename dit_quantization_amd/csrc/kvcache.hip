@@ -11,6 +11,7 @@
 #include "device_common.hpp"
 #include "encode8.hpp"
 #include "fp8_kernels.hpp"
+#include "kv_search.hpp"
 #include "lanes.hpp"
 
 namespace nvfp4 {
@@ -24,39 +25,27 @@ struct Place {
 };
 struct Places {
   Place at[kMaxTokens];
-  int cu[257];  // every step-th entry of the table, so that 256 or fewer sequences are searched in LDS
+  int cu[kCuHeld + 1];  // (256 or fewer sequences are searched in LDS alone)
 };
 
-__device__ __forceinline__ Place locate(const kv8_places& p, const int* cu, int step, int64_t t) {
-  if (t < cu[0] || t >= cu[256]) return {-2, 0};
-  int lo = 0;
-#pragma unroll
-  for (int half = 128; half > 0; half /= 2) lo += cu[lo + half] <= t ? half : 0;  // cu[lo] <= t < cu[lo + half]
-  int first = cu[lo];
-  if (step > 1) {
-    lo *= step;
-    int hi = min(lo + step, (int)p.seqs);
-    while (hi - lo > 1) {  // p.cu[lo] <= t < p.cu[hi]
-      const int mid = lo + (hi - lo) / 2, v = p.cu[mid];
-      if (v <= t) lo = mid, first = v;
-      else hi = mid;
-    }
-  }
-  const int64_t at = t - first + (p.starts ? p.starts[lo] : 0);
+__device__ __forceinline__ Place locate(const kv8_places& p, const int* cu, int64_t t) {
+  int first;
+  const int64_t b = sequence_of(cu, [&](int64_t i) { return p.cu[i]; }, p.seqs, t, first);
+  if (b < 0) return {-2, 0};
+  const int64_t at = t - first + (p.starts ? p.starts[b] : 0);
   if (at < 0 || at >= p.table_width * p.page_size) return {-1, 0};
   const uint32_t slot = (uint32_t)at / (uint32_t)p.page_size;  // at < 2^32
-  const int page = p.page_table[lo * p.table_width + slot];
+  const int page = p.page_table[b * p.table_width + slot];
   return {page >= 0 && page < p.pages ? page : -1, (int)((uint32_t)at - slot * (uint32_t)p.page_size)};
 }
 
 // The places of this workgroup's tokens t0, t0 + 1, ..., and how many it has.
 __device__ __forceinline__ int locate_all(const kv8_places& p, int64_t t0, int per_block, Places& places) {
   const int n = (int)min((int64_t)per_block, p.tokens - t0), k = threadIdx.x;
-  const int step = (int)((p.seqs + 255) / 256);
-  places.cu[k] = p.cu[min((int64_t)k * step, p.seqs)];
-  if (k == 0) places.cu[256] = p.cu[p.seqs];
+  places.cu[k] = p.cu[cu_entry(k, p.seqs)];
+  if (k == 0) places.cu[kCuHeld] = p.cu[p.seqs];
   __syncthreads();
-  if (k < n) places.at[k] = locate(p, places.cu, step, t0 + k);
+  if (k < n) places.at[k] = locate(p, places.cu, t0 + k);
   __syncthreads();
   return n;
 }
