@@ -29,12 +29,12 @@ int tensor_sizes(const kv8_tensor& c, const kv8_places& p) {
 }
 
 // Rows of an output [tokens, heads, dim] that share no element: the wider of the
-// two strides spans all of the narrower one's rows.
+// two strides spans all of the narrower one's rows.  (Products fit: tensor_sizes.)
 bool rows_apart(const kv8_tensor& c, const kv8_places& p) {
   int64_t s0 = p.tokens > 1 ? c.token_stride : INT64_MAX, s1 = p.heads > 1 ? c.head_stride : INT64_MAX;
-  int64_t n0 = p.tokens, n1 = p.heads;
-  if (s0 < s1) std::swap(s0, s1), std::swap(n0, n1);
-  return s1 >= c.dim && (s0 == INT64_MAX || s0 / n1 >= s1);
+  int64_t n1 = p.heads;
+  if (s0 < s1) std::swap(s0, s1), n1 = p.tokens;
+  return s1 >= c.dim && (s0 == INT64_MAX || s0 - c.dim >= (n1 - 1) * s1);
 }
 
 int run(const kv8_tensor* keys, const kv8_tensor* values, const kv8_places* places, int dtype, int q_dtype, bool write,

@@ -76,7 +76,8 @@ typedef struct {
  * heads > 65536, seqs, table_width, tokens, pages or page_size >= 2^31, or more
  * than 2^44 elements of rows: NVFP4_ERR_UNSUPPORTED. No output may overlap an
  * input or another output; rows of kv8_read that overlap each other are
- * NVFP4_ERR_SHAPE.
+ * NVFP4_ERR_SHAPE (so are rows of whose two strides neither spans all that the
+ * other one counts).
  */
 int kv8_write(const kv8_tensor* keys, const kv8_tensor* values, const kv8_places* places, int dtype, int q_dtype,
               void* stream);
