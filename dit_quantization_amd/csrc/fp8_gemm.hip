@@ -20,6 +20,7 @@
 
 #include "device_common.hpp"
 #include "fp8_kernels.hpp"
+#include "fp8_plan.hpp"
 #include "lanes.hpp"
 
 namespace nvfp4 {
@@ -1005,81 +1006,36 @@ hipError_t launch_tile(const Fp8Product& p, hipStream_t stream) {
   });
 }
 
-// 256 x 256: at least two pairs of steps, and rows of y that 32-bit offsets reach.
-hipError_t launch_256(const Fp8Product& p, hipStream_t stream) {
-  if (p.K > 256 && p.y_stride <= 1 << 21) return launch_tile<256, 256, 4, 2, 2, false, true>(p, stream);
-  return launch_tile<128, 256, 2, 4, 3, false, false>(p, stream);
+// One of a plan's kernels.
+hipError_t launch_kernel(Fp8Kernel kernel, const Fp8Product& p, hipStream_t stream) {
+  switch (kernel) {
+    case kRows1x1: return launch_rows<1, 1, 8, 2>(p, stream);
+    case kRows1x2: return launch_rows<1, 2, 4, 2>(p, stream);
+    case kRows2x1: return launch_rows<2, 1, 4, 4>(p, stream);
+    case kRows2x2Of8: return launch_rows<2, 2, 8, 2>(p, stream);
+    case kRows2x2Of4: return launch_rows<2, 2, 4, 2>(p, stream);
+    case kTile32x64: return launch_pipe<32, 64, 1, 2, 5, false>(p, stream);
+    case kTile64x64:
+      return p.bf16 ? launch_pipe<64, 64, 2, 2, 4, false>(p, stream) : launch_pipe<64, 64, 2, 2, 4, true>(p, stream);
+    case kTile64x128:
+      return p.bf16 ? launch_pipe<64, 128, 2, 2, 3, false>(p, stream) : launch_pipe<64, 128, 2, 2, 3, true>(p, stream);
+    case kTile128x128:
+      return p.bf16 ? launch_tile<128, 128, 2, 2, 2, false, false>(p, stream)
+                    : launch_tile<128, 128, 2, 2, 2, true, false>(p, stream);
+    case kTile128x256: return launch_tile<128, 256, 2, 4, 3, false, false>(p, stream);
+    case kTile256x256: return launch_tile<256, 256, 4, 2, 2, false, true>(p, stream);
+    case kNoKernel: break;
+  }
+  return hipErrorInvalidValue;
 }
 
-// Kernels of many rows, and the time of a step (a block of 128 columns of all
-// tiles) of theirs in us: that of the rounds of workgroups that the 256 CUs take,
-// one a CU, or where `both` is given two; measured at K = 4096 and 14336 on M = 32 ..
-// 8192, N = 1024 .. 14336, where the choice is within 8% of the best (us at K =
-// 4096 in the order below, to bf16: 128 x 4096 12.9 / 13.3 / 19.1 / 23.5 / 34.2 / 44.4;
-// 256 x 4096 16.1 / 13.5 / 19.0 / 23.5 / 33.9 / 48.6; 512 x 14336 97 / 70 / 57 / 42.1 /
-// 37.5 / 49.8; 1024 x 4096 56 / 40.4 / 29.7 / 25.0 / 34.2 / 49; 4096 x 4096 202 / 138 /
-// 111 / 78 / 77 / 62.5; to fp32: 512 x 4096 27.8 / 25.6 / 37.2; 2048 x 4096 99.5 / 83.6 /
-// 64.9).
-struct TileKernel {
-  int bm, bn;
-  double alone, both;
-  hipError_t (*launch)(const Fp8Product&, hipStream_t);
-  int64_t tiles_m(int64_t M) const { return (M + bm - 1) / bm; }
-  int64_t tiles_n(int64_t N) const { return (N + bn - 1) / bn; }
-  double step(int64_t M, int64_t N) const {
-    const int64_t t = tiles_m(M) * tiles_n(N);
-    return both > 0 && t > 256 ? (double)((t + 511) / 512) * both : (double)((t + 255) / 256) * alone;
-  }
-};
-const TileKernel kTiles16[] = {{32, 64, 0.30, 0.46, launch_pipe<32, 64, 1, 2, 5, false>},
-                               {64, 64, 0.33, 0.64, launch_pipe<64, 64, 2, 2, 4, false>},
-                               {64, 128, 0.50, 0.88, launch_pipe<64, 128, 2, 2, 3, false>},
-                               {128, 128, 0.66, 1.15, launch_tile<128, 128, 2, 2, 2, false, false>},
-                               {128, 256, 1.07, 0.0, launch_tile<128, 256, 2, 4, 3, false, false>},
-                               {256, 256, 1.80, 0.0, launch_256}};
-const TileKernel kTiles32[] = {{64, 64, 0.47, 0.78, launch_pipe<64, 64, 2, 2, 4, true>},
-                               {64, 128, 0.73, 1.30, launch_pipe<64, 128, 2, 2, 3, true>},
-                               {128, 128, 1.15, 2.00, launch_tile<128, 128, 2, 2, 2, true, false>}};
-
-// The kernel of the least estimated time, or two: whole rounds of one with one
-// workgroup a CU for the first columns or rows and the best for the rest, where
-// that looks 5% better or more (1000 x 20000 x 4096: 1.2 rounds of 256 x 256 tiles
-// 119 us, one round and one of 128 x 128 88; 6000 x 4096 x 4096 107 and 99; 4096 x
-// 14336 x 4096, 3.5 rounds, 226 and 224: the clock is at its power limit. Two
-// workgroups a CU do not end together: 2048 x 14336 x 4096 to fp32 245 and 255).
-hipError_t launch_tiled(const Fp8Product& p, hipStream_t stream) {
-  const TileKernel* all = p.bf16 ? kTiles16 : kTiles32;
-  const int n = p.bf16 ? 6 : 3;
-  const auto best = [&](int64_t M, int64_t N, double& us) {
-    const TileKernel* b = all;
-    us = b->step(M, N);
-    for (int i = 1; i < n; ++i)
-      if (const double t = all[i].step(M, N); t < us) us = t, b = all + i;
-    return b;
-  };
-  double us;
-  const TileKernel *first = best(p.M, p.N, us), *second = nullptr;
-  int64_t M1 = p.M, N1 = p.N;
-  const double apart = 3.0 * 128 / (double)p.K;  // of a second launch
-  us *= 0.95;
-  for (int i = 0; i < n; ++i) {
-    const TileKernel& k = all[i];
-    const int64_t tm = k.tiles_m(p.M), tn = k.tiles_n(p.N), whole = tm * tn / 256 * 256;
-    if (k.both > 0 || whole == 0) continue;
-    const auto consider = [&](int64_t M, int64_t N, int64_t M2, int64_t N2) {
-      if (M == 0 || N == 0 || M2 <= 0 || N2 <= 0) return;
-      double rest;
-      const TileKernel* b = best(M2, N2, rest);
-      if (const double t = k.step(M, N) + rest + apart; t < us) us = t, first = &k, second = b, M1 = M, N1 = N;
-    };
-    consider(p.M, whole / tm * k.bn, p.M, p.N - whole / tm * k.bn);  // (bn is a multiple of 128)
-    consider(whole / tn * k.bm, p.N, p.M - whole / tn * k.bm, p.N);
-  }
+hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
+  const Fp8Plan plan = fp8_plan(p.M, p.N, p.K, p.bf16);
   Fp8Product a = p;
-  a.M = M1;
-  a.N = (int)N1;
-  if (const hipError_t e = first->launch(a, stream); e != hipSuccess || !second) return e;
-  const int64_t G = (p.K + 127) / 128, m = M1 < p.M ? M1 : 0, c = N1 < p.N ? N1 : 0;
+  a.M = plan.M;
+  a.N = (int)plan.N;
+  if (const hipError_t e = launch_kernel(plan.first, a, stream); e != hipSuccess || plan.second == kNoKernel) return e;
+  const int64_t G = (p.K + 127) / 128, m = plan.M < p.M ? plan.M : 0, c = plan.N < p.N ? plan.N : 0;
   a = p;
   a.M -= m;
   a.N -= (int)c;
@@ -1088,26 +1044,7 @@ hipError_t launch_tiled(const Fp8Product& p, hipStream_t stream) {
   a.w += c * p.K;
   a.ws += c / 128 * G;
   a.y = reinterpret_cast<char*>(p.y) + (m * p.y_stride + c) * (p.bf16 ? 2 : 4);
-  return second->launch(a, stream);
-}
-
-// Few rows in all: workgroups of few waves that share nothing but their sums,
-// as long as there are about two of them a CU at most; from there on tiles
-// through LDS, by their estimated time.
-// (us, K = 4096: M = 16, N = 1024 / 4096 / 14336: rows<1, 1> 4.6 / 6.4 / 17.0, rows<1, 2> 5.7 / 7.5 (8 waves), - / - / 14.6
-// (4); M = 32, N = 4096: rows<2, 1> 7.8, rows<2, 2> 9.9; M = 64, N = 4096: rows<2, 2> of 8 waves 9.8, 32 x 64 tiles 12.2; M =
-// 128, N = 4096: rows<2, 2> of 4 waves 14.3, 32 x 64 tiles 12.6, to fp32 14.3 and 18.9, 64 x 64 tiles 18.1.)
-hipError_t launch_fp8_gemm(const Fp8Product& p, hipStream_t stream) {
-  const auto tiles = [&](int64_t bm, int64_t bn) { return (p.M + bm - 1) / bm * ((p.N + bn - 1) / bn); };
-  if (p.M <= 16) {
-    if (tiles(16, 16) <= 512) return launch_rows<1, 1, 8, 2>(p, stream);
-    return launch_rows<1, 2, 4, 2>(p, stream);
-  }
-  const int64_t t = tiles(32, 16);
-  if (t <= 256) return launch_rows<2, 1, 4, 4>(p, stream);
-  if (t <= 512) return launch_rows<2, 2, 8, 2>(p, stream);
-  if (!p.bf16 && t <= 1024) return launch_rows<2, 2, 4, 2>(p, stream);
-  return launch_tiled(p, stream);
+  return launch_kernel(plan.second, a, stream);
 }
 
 }  // namespace nvfp4

@@ -57,7 +57,7 @@ def test_product_bound(M, N, K, kind):
 
 # every rows kernel, and kernels of many rows; G = 5, 9 and 33: the last blocks of a row are no whole run of any kernel's
 NEIGHBOURS = [(2, 64, 640), (15, 300, 1040), (16, 8300, 656), (16, 4096, 4112), (40, 64, 640), (130, 512, 1040), (33, 5000, 640),
-              (70, 5000, 1040), (300, 264, 640), (390, 1411, 1040), (700, 2056, 656), (513, 5016, 1040), (3300, 9000, 400)]
+              (70, 5000, 1040), (300, 264, 640), (390, 1411, 1040), (700, 2056, 656), (513, 5016, 1040), (3300, 9000, 400), (64, 4096, 1040), (1000, 5000, 656)]
 
 
 @pytest.mark.parametrize("M,N,K", NEIGHBOURS)

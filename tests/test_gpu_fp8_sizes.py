@@ -21,10 +21,14 @@ def sparse(rows, K, hot, seed, rest):
     return t.view(E4), v
 
 
-# bf16: tiles of 32 x 64, 64 x 64, 64 x 128, 128 x 128, 128 x 256, 256 x 256, with short last panels of both operands.
-# To fp32 the second to fourth are 64 x 64, 64 x 128 and 128 x 128.  32768 blocks of columns and, in the last K, 32767.
+# bf16: tiles of 32 x 64, 64 x 64, 64 x 128, 128 x 128, 128 x 256, 256 x 256, with short last panels of both operands, and
+# two launches. To fp32 the second to fourth are 64 x 64, 64 x 128 and 128 x 128.
+LONGEST = [(40, 4200), (390, 1411), (700, 2056), (900, 3500), (1000, 5000), (2900, 4100), (2300, 4100)]
+
+
+# 32768 blocks of columns and, in the last K, 32767
 @pytest.mark.parametrize("K", [1 << 22, (1 << 22) - 16, (1 << 22) - 240])
-@pytest.mark.parametrize("M,N", [(40, 4200), (390, 1411), (700, 2056), (900, 3500), (1000, 5000), (2300, 4100)])
+@pytest.mark.parametrize("M,N", LONGEST)
 def test_longest_rows(M, N, K):
     """K = 2^22 (panels of 256 rows are 2^30 bytes) and a little less: columns at both ends of the rows, at the ends of
     the last blocks, and some between; ones in the weight elsewhere, so that a wrong column of x or of the weight counts."""
