@@ -799,8 +799,9 @@ __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_tile_ke
 
 // Small tiles: the fragments of two blocks fit the registers, so the next
 // block's are read while this one's are multiplied, and a step meets once.
-// 333 x 5000 x 4112 with 64 x 128 tiles, the kernel above and this one: 27.2 and
-// 22.9 us to bf16, 33.7 and 27.8 to fp32.
+// 64 x 128 tiles with the kernel above and with this one: to fp32 333 x 5000 x 4112
+// 28.1 and 25.7 us, 300 x 4096 x 14336 77.7 and 67.2; to bf16 23.1 and 23.0, 512 x 4096
+// x 14336 55.6 and 58.6.
 template <int BM, int BN, int WM, int WN, int NS, bool WIDE>
 __global__ __launch_bounds__(WM * WN * 64)
 __attribute__((amdgpu_waves_per_eu(WM * WN >= 4 ? 2 : 1))) void fp8_gemm_pipe_kernel(Fp8Product p) {

@@ -30,13 +30,16 @@ struct Fp8Plan {
 
 // Kernels of many rows, and the time of a step (a block of 128 columns of all
 // tiles) of theirs in us: that of the rounds of workgroups that the 256 CUs take,
-// one a CU, or where `both` is given two; measured at K = 4096 and 14336 on M = 32 ..
-// 8192, N = 1024 .. 14336, where the choice is within 8% of the best (us at K =
-// 4096 in the order below, to bf16: 128 x 4096 12.9 / 13.3 / 19.1 / 23.5 / 34.2 / 44.4;
-// 256 x 4096 16.1 / 13.5 / 19.0 / 23.5 / 33.9 / 48.6; 512 x 14336 97 / 70 / 57 / 42.1 /
-// 37.5 / 49.8; 1024 x 4096 56 / 40.4 / 29.7 / 25.0 / 34.2 / 49; 4096 x 4096 202 / 138 /
-// 111 / 78 / 77 / 62.5; to fp32: 512 x 4096 27.8 / 25.6 / 37.2; 2048 x 4096 99.5 / 83.6 /
-// 64.9).
+// one a CU, or where `both` is given two.  Of 333 sizes (M = 32 .. 8192, N = 1024, 4096,
+// 5000, 14336, K = 1024, 4096, 14336, either output) the choice was within 8% of the
+// fastest kernel in 318 and within 15% in 329; in the other four, up to 31% slower
+// (2048 x 5000 x 14336 to fp32 400 us, with 128 x 128 tiles 306), half or less of a last
+// round of two a CU counts as a full one.  us at K = 4096 in the order below, to bf16:
+// 128 x 4096 12.3 / 11.8 / 15.5 / 20.9 / 29.0 / 41.3; 256 x 4096 14.5 / 12.2 / 15.7 / 21.0 /
+// 29.1 / 43.6; 512 x 14336 98 / 70 / 57 / 42.8 / 36.7 / 51.0; 1024 x 4096 52 / 35.3 / 26.5 /
+// 23.5 / 31.6 / 45.5; 4096 x 4096 208 / 129 / 103 / 76 / 74 / 61.1; to fp32: 512 x 4096 26.6 /
+// 24.1 / 35.3; 2048 x 4096 96.8 / 76.9 / 65.7.  (From K = 4096 to 14336 a step of a full
+// round takes 0.3 / 0.35 / 0.54 / 0.66 / 1.0 / 1.7, to fp32 0.48 / 0.7 / 1.08.)
 struct Fp8Tiles {
   Fp8Kernel kernel;
   int bm, bn;

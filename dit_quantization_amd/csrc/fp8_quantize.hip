@@ -14,10 +14,11 @@ namespace nvfp4 {
 
 // ---- weights.  A workgroup of 256 threads has one block: 16 lanes a row of
 // 128 columns (8 each), 16 rows at a time, 8 vectors a thread, so that a block
-// is read once.  14336 x 4096: fp32 51.6 us, 5.7 TB/s, bf16 34 us, 5.2 TB/s:
-// memory.  About a block a CU (1100 x 4112, 8 us): the latency of one load and
-// some 900 instructions behind it, which more threads a block do not shorten
-// (512 and 1024: 8.2 and 8.3 us; bf16 14336 x 4096 34.5 and 40).
+// is read once.  14336 x 4096: fp32 51.4 us, 5.7 TB/s, bf16 33.8 us, 5.2 TB/s:
+// memory.  About a block a CU (1100 x 4112, 7.7 us): the latency of one load and
+// some 900 instructions behind it, which more threads a block hardly shorten
+// (kernels alone, without the binding: 128, 256, 512 and 1024 threads 10.1, 7.7,
+// 7.4 and 7.6 us; bf16 14336 x 4096 38.5, 33.8, 33.9 and 38.5).
 template <bool BF>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(const void* __restrict__ x, int64_t stride, int64_t rows,
                                                            int cols, int blocks_k, uint8_t* __restrict__ codes,

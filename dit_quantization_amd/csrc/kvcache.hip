@@ -5,8 +5,9 @@
 // token finds its place (a search in cu and one page number), then all threads
 // move the tokens' heads, several vectors in flight each.  Memory bounds both
 // where there are many tokens (65536 tokens of 8 heads of 128, bf16: written
-// in 91 us, 4.5 TB/s, read in 87, 4.7), and below about a thousand the launch
-// and the three reads that follow each other (cu, page number, codes): 4.5 us.
+// in 92 to 95 us, 4.3 to 4.4 TB/s, read in 87, 4.7; fp32 written in 138, 4.9, read in
+// 194, 3.5), and below about a thousand the launch and the three reads that
+// follow each other (cu, page number, codes): 4.5 us.
 // (Every thread finding its own place and moving one vector: 137 us.)
 #include "device_common.hpp"
 #include "encode8.hpp"
