@@ -83,7 +83,7 @@ def test_rows_do_not_meet(M, N, K, bad):
             assert not bool(torch.isfinite(got[1::2]).any())
 
 
-def fastest(calls, rounds=7):
+def fastest(calls, rounds=13):
     """The shortest time of each call among others of its kind (us), taken in turn."""
     best = [float("inf")] * len(calls)
     for r in range(rounds):
